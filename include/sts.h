@@ -65,7 +65,7 @@ typedef enum {
   STS_ERR_SHAPE = 2,            /* T, d, V, chunk sizes, alignment, or a
                                    metadata length != T (validated, never
                                    truncated: "Self-review pass") */
-  STS_ERR_DTYPE = 3,            /* operand dtype other than bf16 (binding) */
+  STS_ERR_DTYPE = 3,            /* a dtype that the entry point does not take */
   STS_ERR_TEMPERATURE = 4,      /* some row has tau not finite or <= 0 */
   STS_ERR_TOP_K = 5,            /* reserved: every int32 top_k is valid */
   STS_ERR_TOP_P = 6,            /* some row has top_p not in (0, 1] */
@@ -111,6 +111,11 @@ typedef struct {
 #define STS_ROW_TARGET_IN_SUPPORT 1 /* y in S */
 #define STS_ROW_INVALID 2           /* row failed validation */
 #define STS_ROW_IDENTITY 4          /* no active filter */
+/* sts_token_logprobs only */
+#define STS_ROW_EMPTY 8            /* every logit is -inf: nothing is left */
+#define STS_ROW_BAD_TEMPERATURE 16 /* why a row is STS_ROW_INVALID */
+#define STS_ROW_BAD_TARGET 32
+#define STS_ROW_BAD_LOGIT 64
 
 /* Bytes of workspace needed. pass: 0 forward (also sts_sample), 1 backward,
  * 2 sts_filter_logits. Returns 0 for an invalid shape. */
@@ -348,6 +353,128 @@ sts_status sts_policy_grad(int64_t T, const float* logprob, const float* old_log
                            const float* advantage, int objective, float eps_low, float eps_high,
                            float scale, float* grad_logprob, sts_stream_t stream);
 
+/* Element types of the entry points that take more than one. */
+typedef enum {
+  STS_DTYPE_F32 = 0,
+  STS_DTYPE_BF16 = 1,
+  STS_DTYPE_F16 = 2,
+  STS_DTYPE_E4M3 = 3, /* 8-bit, 4 exponent bits, largest 448, no infinity */
+  STS_DTYPE_E5M2 = 4  /* 8-bit, 5 exponent bits, largest 57344 */
+} sts_dtype;
+
+/* A head kept in 8 bits: x [R, K] as 8-bit codes q and one fp32 scale per block
+ * of block_rows x 128 elements (block_rows 1 or 128; blocks at the edges are
+ * smaller), x ~ q * scale:
+ *   scale = a / top, a the largest finite |x| of the block, top the largest
+ *           code (448 for e4m3, 57344 for e5m2); 1 where that quotient is 0
+ *   q     = x / scale (IEEE fp32 division), limited to +-top, rounded to
+ *           nearest even; NaN where x is not finite
+ * x_dtype: STS_DTYPE_F32, _BF16 or _F16; element (r, k) at x[r * stride_r + k *
+ * stride_k], one of the strides 1 (a transposed view has stride_r == 1), the
+ * other at least the extent it steps over. q_dtype: STS_DTYPE_E4M3 or _E5M2;
+ * q's rows are q_ld >= K bytes apart (sts_block_scaled_product wants a
+ * multiple of 16), bytes past K are left as they are. scale [ceil(R /
+ * block_rows)][scale_ld >= ceil(K / 128)]. R = 0 is allowed (nothing is
+ * written). Asynchronous, allocates nothing, one kernel launch.
+ * STS_ERR_DTYPE, STS_ERR_SHAPE, STS_ERR_NULL. */
+sts_status sts_block_quantize(int64_t R, int64_t K, const void* x, int x_dtype, int64_t stride_r,
+                              int64_t stride_k, int block_rows, int q_dtype, void* q,
+                              int64_t q_ld, float* scale, int64_t scale_ld, sts_stream_t stream);
+
+/* A matrix [rows, K] in 8 bits with its scales, as sts_block_quantize writes
+ * it. q: rows of 8-bit codes, ld >= K bytes apart; q and ld multiples of 16
+ * bytes. Element (r, kb) of the scales at scale[(r / block_rows) *
+ * scale_stride_r + kb * scale_stride_k], any strides >= 0. */
+typedef struct {
+  const void* q;
+  int dtype; /* STS_DTYPE_E4M3 or _E5M2 */
+  int64_t rows, ld;
+  const float* scale;
+  int64_t scale_stride_r, scale_stride_k;
+  int block_rows; /* 1, or 128 (B only) */
+} sts_block_operand;
+
+/* C [M, N] = A [M, K] . B [N, K]^T, each block of 128 along K scaled in fp32:
+ *   C[m, n] = sum_kb a[m, kb] b[n, kb] sum_{k in kb} A[m, k] B[n, k]
+ * (tensor-core products and sums of a block in fp32, blocks summed in fp32
+ * registers in increasing k), then divided by temperature[m] where that is
+ * given (IEEE fp32 division, not validated: sts_resolve_logits and
+ * sts_token_logprobs check the rows' temperatures), then added to C where
+ * accumulate is set (fp32 C only), then rounded to c_dtype (STS_DTYPE_F32 or
+ * _BF16). With the hidden states as A and a head [V, d] as B it is the 8-bit
+ * counterpart of sts_scaled_logits; the logits' gradient as A and the
+ * transposed head as B give dH; the transposed gradient as A and the
+ * transposed hidden states as B give dW. C's rows are ldc elements apart. It
+ * must not overlap A, B or the scales. M = 0 and N = 0 are allowed. One kernel
+ * launch, no scratch memory: ws may be NULL, or 256 bytes for the status word
+ * that sts_get_status reads (STS_ERR_TIMEOUT); without it a device-side wait
+ * that gave up is not reported. The result depends on the shapes and the
+ * device's SM count, not on what else runs. */
+sts_status sts_block_scaled_product(const sts_block_operand* A, const sts_block_operand* B,
+                                    int64_t K, const float* temperature, void* C, int c_dtype,
+                                    int64_t ldc, int accumulate, void* ws, size_t ws_bytes,
+                                    sts_stream_t stream);
+
+/* Rows of logits and the tokens that are asked of them. */
+typedef struct {
+  const void* logits;       /* [T][ld], the first V of each row, element-aligned */
+  int dtype;                /* STS_DTYPE_F32, _BF16 or _F16 */
+  int64_t T, V, ld;         /* T >= 0, V >= 1, ld >= V */
+  const int64_t* tokens;    /* [T][tokens_ld], the first m of each row; -1: none */
+  int64_t m, tokens_ld;     /* 0 <= m <= 512 */
+  const float* temperature; /* [T] finite, > 0; NULL: 1 */
+  int64_t top_n;            /* alternatives per row, 0 <= top_n <= 64 */
+} sts_token_rows;
+
+/* What sts_token_logprobs writes beside the log probabilities; any pointer may
+ * be NULL there (top_id and top_logprob only where top_n is 0). */
+typedef struct {
+  float* logit_max;   /* [T] M, the largest logit */
+  float* log_sum;     /* [T] ln sum_i exp((z_i - M) / tau) */
+  float* lse;         /* [T] M / tau + log_sum */
+  float* entropy;     /* [T] nats */
+  int32_t* flags;     /* [T] 0, STS_ROW_EMPTY, or STS_ROW_INVALID and a STS_ROW_BAD_* */
+  int64_t* top_id;    /* [T][top_n] in (logit descending, id ascending) order */
+  float* top_logprob; /* [T][top_n] */
+} sts_token_stats;
+
+/* Log probabilities of given tokens under softmax(z / tau) over the whole row
+ * (no support program: sts_resolve_logits is the filtered form), logprob [T][m]
+ * = (z_y - M) / tau - log_sum, with the row's logsumexp, entropy and top_n
+ * alternatives from the same single pass over the logits.
+ *   - A token of -1 is no token: its logprob is 0. A masked one (its logit is
+ *     -inf) has -inf.
+ *   - Masked tokens are never alternatives: where fewer than top_n are left,
+ *     the rest have id -1 and -inf. Finite logits of any size (the type's
+ *     lowest value as a mask) count as what they are.
+ *   - A row of nothing but -inf (STS_ROW_EMPTY): logprob, lse, log_sum and M
+ *     -inf, entropy 0, no alternatives.
+ *   - A row with a bad temperature, a token outside [-1, V), or a logit that is
+ *     NaN or +inf is invalid: its floating results are NaN, its ids -1, its
+ *     flags say why; other rows are unaffected. There is no status word.
+ * Sums in fp32 per thread, joined in float64. Asynchronous, allocates nothing,
+ * one kernel launch; calls share nothing and may overlap. T = 0 is allowed. */
+sts_status sts_token_logprobs(const sts_token_rows* rows, float* logprob,
+                              const sts_token_stats* stats, sts_stream_t stream);
+
+/* The gradient of those results: for dL/dlogprob = grad_logprob [T][m],
+ * dL/dentropy = grad_entropy [T] and dL/dtop_logprob = grad_top [T][top_n]
+ * (each may be NULL),
+ *   dlogits_i = (1/tau) (sum_{j: y_j = i} g_j - p_i (G + h (ln p_i + entropy)))
+ * with G the sum of the g_j (alternatives included) whose token has a finite
+ * logit: tokens of -1 and masked tokens take no part. The same token given
+ * more than once gets the sum, in a fixed order. Empty and invalid rows get
+ * zeros. rows is the forward's; of `saved` logit_max, log_sum and flags are
+ * read, entropy where grad_entropy is given, top_id where grad_top is.
+ * dlogits [T][dlogits_ld] in STS_DTYPE_F32, _BF16 or _F16 (entries past V are
+ * left as they are); it may be the logits themselves (same pointer, type and
+ * stride), not a part of them (STS_ERR_SHAPE). Asynchronous, allocates nothing,
+ * one kernel launch. */
+sts_status sts_token_logprobs_backward(const sts_token_rows* rows, const sts_token_stats* saved,
+                                       const float* grad_logprob, const float* grad_entropy,
+                                       const float* grad_top, void* dlogits, int dlogits_dtype,
+                                       int64_t dlogits_ld, sts_stream_t stream);
+
 const char* sts_status_string(sts_status status);
 
 /* Kernel kinds for the launch counters and the timing facility below. */
@@ -358,7 +485,11 @@ typedef enum {
   STS_KERNEL_DZ_GEMM = 3,     /* backward recompute, dz epilogue */
   STS_KERNEL_DW_GEMM = 4,     /* dW slice = dZ^T . H */
   STS_KERNEL_DH_GEMM = 5,     /* dH (+)= dZ . W slice */
-  STS_KERNEL_KINDS = 6
+  STS_KERNEL_BLOCK_QUANTIZE = 6,  /* sts_block_quantize */
+  STS_KERNEL_BLOCK_PRODUCT = 7,   /* sts_block_scaled_product */
+  STS_KERNEL_TOKEN_LOGPROBS = 8,  /* sts_token_logprobs */
+  STS_KERNEL_TOKEN_GRAD = 9,      /* sts_token_logprobs_backward */
+  STS_KERNEL_KINDS = 10
 } sts_kernel_kind;
 
 /* Number of kernels of a kind this process has launched through the library

@@ -46,6 +46,10 @@ __all__ = [
     "sts_filter_logits",
     "sts_scaled_logits",
     "sts_policy_grad",
+    "sts_block_quantize",
+    "sts_block_scaled_product",
+    "sts_token_logprobs",
+    "sts_token_logprobs_backward",
     "sts_get_status",
     "sts_path_counts",
     "sts_status_string",
@@ -58,6 +62,10 @@ __all__ = [
     "ROW_TARGET_IN_SUPPORT",
     "ROW_INVALID",
     "ROW_IDENTITY",
+    "ROW_EMPTY",
+    "ROW_BAD_TEMPERATURE",
+    "ROW_BAD_TARGET",
+    "ROW_BAD_LOGIT",
     "EXPORTED_SYMBOLS",
 ]
 
@@ -68,12 +76,19 @@ STS_OK = 0
 STS_ERR_NULL = 1
 STS_ERR_SHAPE = 2
 STS_ERR_DTYPE = 3
+STS_ERR_TEMPERATURE = 4
+STS_ERR_TARGET = 8
 STS_ERR_WORKSPACE = 9
 ROW_TARGET_IN_SUPPORT = 1
 ROW_INVALID = 2
 ROW_IDENTITY = 4
+ROW_EMPTY = 8
+ROW_BAD_TEMPERATURE = 16
+ROW_BAD_TARGET = 32
+ROW_BAD_LOGIT = 64
 
-KERNEL_KINDS = ("validate", "logits_gemm", "resolve", "dz_gemm", "dw_gemm", "dh_gemm")
+KERNEL_KINDS = ("validate", "logits_gemm", "resolve", "dz_gemm", "dw_gemm", "dh_gemm",
+                "block_quantize", "block_product", "token_logprobs", "token_grad")
 
 EXPORTED_SYMBOLS = (
     "sts_workspace_bytes",
@@ -102,6 +117,10 @@ EXPORTED_SYMBOLS = (
     "sts_tp_count",
     "sts_tp_exact",
     "sts_tp_finish",
+    "sts_block_quantize",
+    "sts_block_scaled_product",
+    "sts_token_logprobs",
+    "sts_token_logprobs_backward",
 )
 
 
@@ -131,6 +150,26 @@ class _Saved(ctypes.Structure):
     _fields_ = [("row_max", ctypes.c_void_p), ("lse_support", ctypes.c_void_p),
                 ("cut_logit", ctypes.c_void_p), ("cut_id", ctypes.c_void_p),
                 ("support_size", ctypes.c_void_p), ("flags", ctypes.c_void_p)]
+
+
+class _BlockOperand(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("dtype", ctypes.c_int), ("rows", ctypes.c_int64),
+                ("ld", ctypes.c_int64), ("scale", ctypes.c_void_p),
+                ("scale_stride_r", ctypes.c_int64), ("scale_stride_k", ctypes.c_int64),
+                ("block_rows", ctypes.c_int)]
+
+
+class _TokenRows(ctypes.Structure):
+    _fields_ = [("logits", ctypes.c_void_p), ("dtype", ctypes.c_int), ("T", ctypes.c_int64),
+                ("V", ctypes.c_int64), ("ld", ctypes.c_int64), ("tokens", ctypes.c_void_p),
+                ("m", ctypes.c_int64), ("tokens_ld", ctypes.c_int64),
+                ("temperature", ctypes.c_void_p), ("top_n", ctypes.c_int64)]
+
+
+class _TokenStats(ctypes.Structure):
+    _fields_ = [("logit_max", ctypes.c_void_p), ("log_sum", ctypes.c_void_p),
+                ("lse", ctypes.c_void_p), ("entropy", ctypes.c_void_p), ("flags", ctypes.c_void_p),
+                ("top_id", ctypes.c_void_p), ("top_logprob", ctypes.c_void_p)]
 
 
 _lib = None
@@ -213,6 +252,18 @@ def load():
     lib.sts_filter_logits_noalloc.argtypes = [ctypes.POINTER(_Shape), P, ctypes.POINTER(_Rows), P, P,
                                               P, P, P]
     lib.sts_filter_logits_noalloc.restype = ctypes.c_int
+    I = ctypes.c_int
+    lib.sts_block_quantize.argtypes = [I64, I64, P, I, I64, I64, I, I, P, I64, P, I64, P]
+    lib.sts_block_quantize.restype = ctypes.c_int
+    lib.sts_block_scaled_product.argtypes = [ctypes.POINTER(_BlockOperand),
+                                             ctypes.POINTER(_BlockOperand), I64, P, P, I, I64, I, P,
+                                             S, P]
+    lib.sts_block_scaled_product.restype = ctypes.c_int
+    lib.sts_token_logprobs.argtypes = [ctypes.POINTER(_TokenRows), P, ctypes.POINTER(_TokenStats), P]
+    lib.sts_token_logprobs.restype = ctypes.c_int
+    lib.sts_token_logprobs_backward.argtypes = [ctypes.POINTER(_TokenRows),
+                                                ctypes.POINTER(_TokenStats), P, P, P, P, I, I64, P]
+    lib.sts_token_logprobs_backward.restype = ctypes.c_int
     lib.sts_abi_version.argtypes = []
     lib.sts_abi_version.restype = ctypes.c_int
     _lib = lib
@@ -740,3 +791,289 @@ def sts_gather_vocab_shards(src, dst, *, stream=None):
     _check(lib.sts_gather_vocab_shards(_ptr(src), world, T, Vl, _ptr(dst), dst.shape[1],
                                        _stream(stream)), "sts_gather_vocab_shards")
     return dst
+
+
+# ---------------------------------------------------------------- an 8-bit head, token logprobs
+
+_F32, _BF16, _F16 = torch.float32, torch.bfloat16, torch.float16
+_E4M3, _E5M2 = torch.float8_e4m3fn, torch.float8_e5m2
+_DTYPE_CODE = {_F32: 0, _BF16: 1, _F16: 2, _E4M3: 3, _E5M2: 4}
+_BLOCK = 128
+
+
+class _Call:
+    """Where one call runs: the tensors' device (made current for the call if it is not) and
+    the given stream, or the device's current one. Outputs are allocated on that stream; with
+    an explicit stream the inputs are recorded on it, so that freeing them early is safe."""
+
+    def __init__(self, stream, *tensors):
+        dev = None
+        for name, t in tensors:
+            if t is None:
+                continue
+            if not t.is_cuda:
+                raise StsError(STS_ERR_SHAPE, f"{name} must be a CUDA tensor")
+            if dev is None:
+                dev = t.device
+            elif t.device != dev:
+                raise StsError(STS_ERR_SHAPE, f"{name} is on {t.device}, expected {dev}")
+        self.device = dev
+        self.contexts = ()
+        if dev.index != torch.cuda.current_device():
+            self.contexts = (torch.cuda.device(dev),)
+        if stream is None:
+            self.stream = torch.cuda.current_stream(dev).cuda_stream
+        else:
+            if stream.device != dev:
+                raise StsError(STS_ERR_SHAPE, f"the stream is on {stream.device}, expected {dev}")
+            self.stream = stream.cuda_stream
+            self.contexts += (torch.cuda.stream(stream),)
+            for _, t in tensors:
+                if t is not None:
+                    t.record_stream(stream)
+
+    def __enter__(self):
+        for c in self.contexts:
+            c.__enter__()
+        return self
+
+    def __exit__(self, *exc):
+        for c in reversed(self.contexts):
+            c.__exit__(*exc)
+
+
+def _float_code(t, name, allowed=(_F32, _BF16, _F16)):
+    if t.dtype not in allowed:
+        raise StsError(STS_ERR_DTYPE, f"{name} must be one of {allowed}, got {t.dtype}")
+    return _DTYPE_CODE[t.dtype]
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def sts_block_quantize(x, *, block_rows=1, dtype=_E4M3, q=None, scale=None, stream=None):
+    """x [R, K] (fp32, bf16 or fp16; contiguous rows, or a transposed view of them) as 8-bit codes
+    and one fp32 scale per ``block_rows`` x 128 block (``block_rows`` 1 or 128).
+
+    Returns ``(q [R, K], scale [ceil(R / block_rows), ceil(K / 128)])`` with x ~ q * scale.
+    ``q``'s rows are a multiple of 16 bytes apart, as ``sts_block_scaled_product`` wants them
+    (a view where K is no multiple of 16). ``q`` and ``scale`` may be given to be written."""
+    lib = load()
+    if dtype not in (_E4M3, _E5M2):
+        raise StsError(STS_ERR_DTYPE, f"dtype must be an 8-bit float, got {dtype}")
+    if x.dim() != 2:
+        raise StsError(STS_ERR_SHAPE, "x must be [R, K]")
+    code = _float_code(x, "x")
+    if block_rows not in (1, _BLOCK):
+        raise StsError(STS_ERR_SHAPE, f"block_rows must be 1 or {_BLOCK}, got {block_rows}")
+    R, K = x.shape
+    sr, sk = x.stride()
+    if K == 1 or (R > 1 and sk != 1 and sr != 1):
+        # one column is a row-contiguous matrix of any row stride
+        if K != 1:
+            raise StsError(STS_ERR_SHAPE, "x must have unit stride along its rows or columns")
+        sk = 1
+        sr = max(sr, 1)
+    elif R == 1 and sk != 1:
+        sr = 1  # one row of strided columns: a transposed view
+    with _Call(stream, ("x", x), ("q", q), ("scale", scale)) as call:
+        blocks = (-(-R // block_rows), -(-K // _BLOCK))
+        if q is None:
+            q = torch.empty((R, -(-K // 16) * 16), dtype=dtype, device=call.device)
+            if q.shape[1] != K:
+                q = q[:, :K]
+        elif q.dtype != dtype or q.shape != x.shape or (K > 1 and q.stride(1) != 1):
+            raise StsError(STS_ERR_SHAPE, f"q must be {dtype} {tuple(x.shape)} with contiguous rows")
+        if scale is None:
+            scale = torch.empty(blocks, dtype=_F32, device=call.device)
+        elif scale.dtype != _F32 or scale.shape != blocks or (blocks[1] > 1 and scale.stride(1) != 1):
+            raise StsError(STS_ERR_SHAPE, f"scale must be fp32 {blocks} with contiguous rows")
+        st = lib.sts_block_quantize(R, K, x.data_ptr(), code, sr, sk, block_rows, _DTYPE_CODE[dtype],
+                                    q.data_ptr(), q.stride(0) if R > 1 else K, scale.data_ptr(),
+                                    scale.stride(0) if blocks[0] > 1 else blocks[1], call.stream)
+    _check(st, "sts_block_quantize")
+    return q, scale
+
+
+def _block_operand(q, scale, name, rows_only):
+    if q.dtype not in (_E4M3, _E5M2):
+        raise StsError(STS_ERR_DTYPE, f"{name} must be float8_e4m3fn or float8_e5m2, got {q.dtype}")
+    if q.dim() != 2 or (q.shape[1] > 1 and q.stride(1) != 1):
+        raise StsError(STS_ERR_SHAPE, f"{name} must be 2-D with contiguous rows")
+    rows, K = q.shape
+    kb = -(-K // _BLOCK)
+    if scale.dtype != _F32:
+        raise StsError(STS_ERR_DTYPE, f"{name}'s scale must be {_F32}, got {scale.dtype}")
+    block_rows = 1
+    if scale.shape != (rows, kb):
+        block_rows = _BLOCK
+        if rows_only or scale.shape != (-(-rows // _BLOCK), kb):
+            raise StsError(STS_ERR_SHAPE, f"{name}'s scale has shape {tuple(scale.shape)}, expected "
+                                          f"{(rows, kb)}" + ("" if rows_only else
+                                                             f" or {(-(-rows // _BLOCK), kb)}"))
+    ld = q.stride(0) if rows > 1 else -(-K // 16) * 16
+    return _BlockOperand(q.data_ptr(), _DTYPE_CODE[q.dtype], rows, ld, scale.data_ptr(),
+                         scale.stride(0), scale.stride(1), block_rows)
+
+
+def sts_block_scaled_product(A, a_scale, B, b_scale, *, temperature=None, out=None, out_dtype=None,
+                             accumulate=False, ws=None, stream=None, check=False):
+    """C [M, N] = A [M, K] . B [N, K]^T of 8-bit matrices with their scales (``sts_block_quantize``):
+    ``a_scale`` [M, ceil(K / 128)], ``b_scale`` [N, ceil(K / 128)] or [ceil(N / 128), ceil(K / 128)].
+
+    Each block of 128 is summed on the tensor cores and scaled in fp32. The rows are divided by
+    ``temperature`` [M] where it is given (the scaled logits of an 8-bit head). C is ``out`` or new,
+    fp32 (default) or bf16; with ``accumulate`` the product is added to ``out`` (fp32). With
+    ``check`` the call synchronises and raises if a device-side wait gave up."""
+    lib = load()
+    a = _block_operand(A, a_scale, "A", True)
+    b = _block_operand(B, b_scale, "B", False)
+    M, K = A.shape
+    N = B.shape[0]
+    if B.shape[1] != K:
+        raise StsError(STS_ERR_SHAPE, f"A has {K} columns, B {B.shape[1]}")
+    if temperature is not None:
+        if temperature.dtype != _F32 or temperature.shape != (M,) or not temperature.is_contiguous():
+            raise StsError(STS_ERR_SHAPE, f"temperature must be contiguous fp32 {(M,)}")
+    if accumulate and out is None:
+        raise StsError(STS_ERR_NULL, "accumulate needs an out tensor")
+    with _Call(stream, ("A", A), ("a_scale", a_scale), ("B", B), ("b_scale", b_scale),
+               ("temperature", temperature), ("out", out), ("ws", ws)) as call:
+        if out is None:
+            out = torch.empty((M, N), dtype=out_dtype or _F32, device=call.device)
+        elif (out_dtype is not None and out.dtype != out_dtype) or out.shape != (M, N) or (
+                N > 1 and out.stride(1) != 1):
+            raise StsError(STS_ERR_SHAPE, f"out must be {out_dtype or 'fp32 or bf16'} {(M, N)} with "
+                                          "contiguous rows")
+        code = _float_code(out, "out", (_F32, _BF16))
+        if check and ws is None:
+            ws = torch.empty(256, dtype=torch.uint8, device=call.device)
+        st = lib.sts_block_scaled_product(
+            ctypes.byref(a), ctypes.byref(b), K, _at(temperature), out.data_ptr(), code,
+            out.stride(0) if M > 1 else N, 1 if accumulate else 0, _at(ws),
+            0 if ws is None else ws.numel() * ws.element_size(), call.stream)
+        _check(st, "sts_block_scaled_product")
+        if check:
+            sts_get_status(ws, stream, raise_on_error=True)
+    return out
+
+
+def _token_rows(logits, tokens, temperature, top_n):
+    """The C view of the rows; tokens [T] are [T, 1]."""
+    code = _float_code(logits, "logits")
+    if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise StsError(STS_ERR_SHAPE, "logits must be [T, V] with contiguous rows")
+    T, V = logits.shape
+    m = tokens_ld = 0
+    if tokens is not None:
+        if tokens.dtype != torch.int64:
+            raise StsError(STS_ERR_SHAPE, f"tokens must be {torch.int64}, got {tokens.dtype}")
+        if tokens.dim() not in (1, 2) or tokens.shape[0] != T:
+            raise StsError(STS_ERR_SHAPE, f"tokens has shape {tuple(tokens.shape)}, expected "
+                                          f"({T},) or ({T}, m)")
+        m = 1 if tokens.dim() == 1 else tokens.shape[1]
+        tokens_ld = tokens.stride(0) if T > 1 else m
+        if tokens.dim() == 2 and m > 1 and tokens.stride(1) != 1:
+            raise StsError(STS_ERR_SHAPE, "tokens must have contiguous rows")
+    if temperature is not None:
+        if temperature.dtype != _F32 or temperature.shape != (T,) or not temperature.is_contiguous():
+            raise StsError(STS_ERR_SHAPE, f"temperature must be contiguous fp32 {(T,)}")
+    return _TokenRows(logits.data_ptr(), code, T, V, logits.stride(0) if T > 1 else V, _at(tokens), m,
+                      tokens_ld, _at(temperature), int(top_n))
+
+
+def sts_token_logprobs(logits, tokens=None, *, temperature=None, top_n=0, entropy=False, stream=None,
+                       check=False):
+    """Log probabilities of the given tokens under softmax(logits / temperature), one pass over the
+    logits [T, V] (fp32, bf16 or fp16, any row stride).
+
+    ``tokens`` int64 [T] or [T, m] (m <= 512, -1: no token); ``temperature`` fp32 [T] (default 1).
+    Returns ``(logprob, saved)``: logprob fp32 of tokens' shape (None without tokens), and a dict of
+    ``lse``, ``logit_max``, ``log_sum`` [T] fp32, ``flags`` [T] int32, with ``entropy`` also
+    ``entropy`` [T] (nats), with ``top_n`` (<= 64) also ``top_id`` [T, top_n] int64 and
+    ``top_logprob`` [T, top_n]: the most probable tokens, ties by the lower id, -1 and -inf where
+    fewer are unmasked. Invalid rows give NaN and -1 (``flags``); with ``check`` the call
+    synchronises and raises on them."""
+    lib = load()
+    rows = _token_rows(logits, tokens, temperature, top_n)
+    T, n = rows.T, rows.top_n
+    if n < 0:
+        raise StsError(STS_ERR_SHAPE, f"top_n must be 0 or more, got {n}")
+    with _Call(stream, ("logits", logits), ("tokens", tokens), ("temperature", temperature)) as call:
+        dev = call.device
+        stats = torch.empty((4 if entropy else 3, T), dtype=_F32, device=dev).unbind(0)
+        flags = torch.empty(T, dtype=torch.int32, device=dev)
+        saved = {"lse": stats[0], "logit_max": stats[1], "log_sum": stats[2], "flags": flags}
+        if entropy:
+            saved["entropy"] = stats[3]
+        logprob = top_id = top_logprob = None
+        if tokens is not None:
+            logprob = torch.empty(tokens.shape, dtype=_F32, device=dev)
+        if n:
+            saved["top_id"] = top_id = torch.empty((T, n), dtype=torch.int64, device=dev)
+            saved["top_logprob"] = top_logprob = torch.empty((T, n), dtype=_F32, device=dev)
+        out = _TokenStats(_at(stats[1]), _at(stats[2]), _at(stats[0]),
+                          _at(stats[3]) if entropy else None, _at(flags), _at(top_id),
+                          _at(top_logprob))
+        st = lib.sts_token_logprobs(ctypes.byref(rows), _at(logprob), ctypes.byref(out), call.stream)
+        _check(st, "sts_token_logprobs")
+        if check:
+            if stream is not None:
+                stream.synchronize()
+            bad = torch.nonzero(flags & ROW_INVALID)
+            if bad.numel():
+                row = int(bad[0])
+                why = int(flags[row])
+                raise StsError(STS_ERR_TEMPERATURE if why & ROW_BAD_TEMPERATURE else
+                               STS_ERR_TARGET if why & ROW_BAD_TARGET else STS_ERR_SHAPE,
+                               f"row {row}" + (" has a NaN or +inf logit" if why & ROW_BAD_LOGIT
+                                               else ""))
+    return logprob, saved
+
+
+def sts_token_logprobs_backward(logits, tokens, saved, grad_logprob=None, *, grad_entropy=None,
+                                grad_top=None, temperature=None, out=None, out_dtype=None,
+                                stream=None):
+    """The gradient of ``sts_token_logprobs``'s results with respect to the logits [T, V].
+
+    ``saved`` is the forward's (``logit_max``, ``log_sum``, ``flags``; ``entropy`` for
+    ``grad_entropy`` [T], ``top_id`` for ``grad_top`` [T, top_n]); ``grad_logprob`` has logprob's
+    shape. The result is ``out`` or new, of the logits' type unless ``out_dtype`` says otherwise;
+    ``out`` may be ``logits`` itself. Tokens of -1, masked tokens, and empty or invalid rows
+    contribute nothing."""
+    lib = load()
+    top_id = saved["top_id"] if grad_top is not None else None
+    rows = _token_rows(logits, tokens, temperature, 0 if top_id is None else top_id.shape[1])
+    T, V = rows.T, rows.V
+    for name, t, dtype, shape in (
+            ("logit_max", saved["logit_max"], _F32, (T,)), ("log_sum", saved["log_sum"], _F32, (T,)),
+            ("flags", saved["flags"], torch.int32, (T,)),
+            ("grad_logprob", grad_logprob, _F32, None if tokens is None else tokens.shape),
+            ("grad_entropy", grad_entropy, _F32, (T,)),
+            ("entropy", None if grad_entropy is None else saved["entropy"], _F32, (T,)),
+            ("grad_top", grad_top, _F32, None if top_id is None else top_id.shape),
+            ("top_id", top_id, torch.int64, (T, rows.top_n))):
+        if t is not None and (t.dtype != dtype or t.shape != shape or not t.is_contiguous()):
+            raise StsError(STS_ERR_SHAPE, f"{name} must be contiguous {dtype} "
+                                          f"{None if shape is None else tuple(shape)}, got "
+                                          f"{t.dtype} {tuple(t.shape)}")
+    entropy = None if grad_entropy is None else saved["entropy"]
+    with _Call(stream, ("logits", logits), ("tokens", tokens), ("temperature", temperature),
+               ("logit_max", saved["logit_max"]), ("log_sum", saved["log_sum"]),
+               ("flags", saved["flags"]), ("entropy", entropy), ("top_id", top_id),
+               ("grad_logprob", grad_logprob), ("grad_entropy", grad_entropy), ("grad_top", grad_top),
+               ("out", out)) as call:
+        if out is None:
+            out = torch.empty((T, V), dtype=out_dtype or logits.dtype, device=call.device)
+        elif (out_dtype is not None and out.dtype != out_dtype) or out.shape != (T, V) or (
+                V > 1 and out.stride(1) != 1):
+            raise StsError(STS_ERR_SHAPE, f"out must be {(T, V)} with contiguous rows")
+        code = _float_code(out, "out")
+        stats = _TokenStats(_at(saved["logit_max"]), _at(saved["log_sum"]), None, _at(entropy),
+                            _at(saved["flags"]), _at(top_id), None)
+        st = lib.sts_token_logprobs_backward(
+            ctypes.byref(rows), ctypes.byref(stats), _at(grad_logprob), _at(grad_entropy),
+            _at(grad_top), out.data_ptr(), code, out.stride(0) if T > 1 else V, call.stream)
+    _check(st, "sts_token_logprobs_backward")
+    return out

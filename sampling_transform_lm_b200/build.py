@@ -17,7 +17,8 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libsts.so")
-SOURCES = ["sts_api.cu", "resolver.cu", "noalloc.cu", "policy.cu", "tp.cu"]
+SOURCES = ["sts_api.cu", "resolver.cu", "noalloc.cu", "policy.cu", "tp.cu", "quantize.cu",
+           "blockscale.cu", "logprobs.cu"]
 
 
 def _headers() -> list:

@@ -1,0 +1,920 @@
+// Log probabilities of given tokens, entropy and top alternatives of rows of
+// logits, and their gradient.
+//
+// With z the logits of one row, tau its temperature, M = max_i z_i and
+// d_i = (z_i - M) / tau:
+//   S        = sum_i exp(d_i)
+//   log_sum  = ln S,   lse = M / tau + log_sum
+//   logprob  = d_y - log_sum                        for each given token y
+//   entropy  = ln S - (sum_i exp(d_i) d_i) / S
+//   top n    = the first n tokens in (z descending, id ascending) order
+// and for L with dL/dlogprob_j = g_j, dL/dentropy = h, dL/dtop_j = g'_j:
+//   dL/dz_i  = (1 / tau) [ sum_{j: y_j = i} g_j - p_i (G + h (ln p_i + entropy)) ]
+// where G is the sum of every g_j and g'_j whose token has a probability.
+//
+// One pass over the row in each direction; HBM bounds both. The forward's
+// running sums are taken against a fixed base b instead of a running maximum:
+//   x_i = c (z_i - b),  c = log2(e) / tau,  S' = sum 2^x_i,  S'_1 = sum 2^x_i x_i
+// Any base gives the same quotients, so b is the maximum of the first 4,096 to
+// 8,192 elements and moves only when an element exceeds it by 2^64: the inner
+// loop is a difference, a product, a clamp, an exponential and two sums an
+// element (differences of logits: no temperature overflows them). The
+// clamp at -200 (2^-200 is 0 in fp32) keeps 0 * inf out of S'_1 for masked
+// logits. Each thread's sums (fp32, about V / 256 terms) are joined in float64.
+//
+// The alternatives ride in the same loop: a lower bound of the n-th largest
+// element (the n-th largest of group maxima of the first chunk, tightened as
+// the row goes on) is compared with the maximum of each 4 or 8 elements, and
+// only what lies above it is kept as a 64-bit key (monotone logit bits above
+// the inverted id, so that the order of keys is the order of alternatives).
+// Keys that outgrow the buffer (ascending rows, rows of equal logits) are
+// dropped and the row's share is searched again digit by digit.
+//
+// A row is a thread block's, or, where there are too few rows to fill the
+// GPU, that of a cluster of 2, 4 or 8 blocks, each with a stretch of the
+// vocabulary; the first block joins their results over distributed shared
+// memory. One launch, no workspace, nothing shared between calls.
+#include <cmath>
+
+#include <cooperative_groups.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "sts_internal.h"
+
+namespace sts {
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr int kThreads = 256;
+constexpr int kUnroll = 4;       // 16-byte loads in flight per thread
+constexpr int kMaxTop = 64;      // alternatives per row
+constexpr int kMaxGiven = 512;   // given tokens per row
+constexpr int kMaxParts = 8;     // portable cluster size
+constexpr int kKeyCap = 1024;    // keys kept between two tightenings
+constexpr double kLog2eD = 1.4426950408889634074;
+constexpr double kLn2 = 0.69314718055994530942;
+constexpr float kNegInf = -INFINITY;
+
+// log2(e) / tau, finite for every tau > 0
+__device__ __forceinline__ float exponent_scale(float tau) {
+  return (float)fmin(kLog2eD / (double)tau, 3.402823466e+38);
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// The larger one, NaN where either is NaN.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+
+__device__ __forceinline__ float to_f32(float v) { return v; }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
+__device__ __forceinline__ void from_f32(float v, float& o) { o = v; }
+__device__ __forceinline__ void from_f32(float v, __nv_bfloat16& o) { o = __float2bfloat16_rn(v); }
+__device__ __forceinline__ void from_f32(float v, __half& o) { o = __float2half_rn(v); }
+
+// 16 bytes of logits.
+template <typename T>
+struct Vec {
+  static constexpr int kN = 16 / (int)sizeof(T);
+  uint4 w;
+  __device__ __forceinline__ void load(const T* p) { w = __ldg(reinterpret_cast<const uint4*>(p)); }
+  __device__ __forceinline__ void f32(float (&v)[kN]) const;
+  __device__ __forceinline__ float largest() const;  // NaN where one is NaN
+};
+
+template <>
+__device__ __forceinline__ void Vec<float>::f32(float (&v)[4]) const {
+  v[0] = __uint_as_float(w.x);
+  v[1] = __uint_as_float(w.y);
+  v[2] = __uint_as_float(w.z);
+  v[3] = __uint_as_float(w.w);
+}
+template <>
+__device__ __forceinline__ float Vec<float>::largest() const {
+  return max_nan(max_nan(__uint_as_float(w.x), __uint_as_float(w.y)),
+                 max_nan(__uint_as_float(w.z), __uint_as_float(w.w)));
+}
+template <>
+__device__ __forceinline__ void Vec<__nv_bfloat16>::f32(float (&v)[8]) const {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {  // a bf16 is the upper half of its fp32
+    v[2 * i] = __uint_as_float(u[i] << 16);
+    v[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+  }
+}
+template <>
+__device__ __forceinline__ float Vec<__nv_bfloat16>::largest() const {
+  const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&w);
+  const float2 f = __bfloat1622float2(__hmax2_nan(__hmax2_nan(h[0], h[1]), __hmax2_nan(h[2], h[3])));
+  return max_nan(f.x, f.y);
+}
+template <>
+__device__ __forceinline__ void Vec<__half>::f32(float (&v)[8]) const {
+  const __half2* h = reinterpret_cast<const __half2*>(&w);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __half22float2(h[i]);
+    v[2 * i] = f.x;
+    v[2 * i + 1] = f.y;
+  }
+}
+template <>
+__device__ __forceinline__ float Vec<__half>::largest() const {
+  const __half2* h = reinterpret_cast<const __half2*>(&w);
+  const float2 f = __half22float2(__hmax2_nan(__hmax2_nan(h[0], h[1]), __hmax2_nan(h[2], h[3])));
+  return max_nan(f.x, f.y);
+}
+
+// fp32 bits as an unsigned number of the same order; -0 counts as +0.
+__device__ __forceinline__ uint32_t order_bits(float z) {
+  const uint32_t b = __float_as_uint(z + 0.f);
+  return b ^ (((int32_t)b >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float order_value(uint32_t k) {
+  return __uint_as_float(k ^ ((k & 0x80000000u) ? 0x80000000u : 0xFFFFFFFFu));
+}
+__device__ __forceinline__ uint64_t token_key(float z, uint32_t id) {
+  return ((uint64_t)order_bits(z) << 32) | (uint32_t)~id;
+}
+__device__ __forceinline__ float key_logit(uint64_t k) { return order_value((uint32_t)(k >> 32)); }
+__device__ __forceinline__ uint32_t key_id(uint64_t k) { return ~(uint32_t)k; }
+
+struct FwdArgs {
+  const void* z;
+  int64_t ld;
+  int64_t T;
+  int V, parts, stretch;  // stretch: vocabulary entries per part
+  const int64_t* tokens;
+  int64_t tokens_ld;
+  int m;
+  const float* tau;
+  int n;
+  float* logprob;
+  float *logit_max, *log_sum, *lse, *entropy;
+  int32_t* flags;
+  int64_t* top_id;
+  float* top_logprob;
+};
+
+struct Share {  // what one block found in its stretch
+  double s0, s1;
+  float base;
+  int bad;
+  int found;
+  int pad;
+};
+
+struct FwdSmem {
+  uint64_t keys[kKeyCap];
+  uint64_t top[kMaxTop];
+  uint64_t joined[kMaxParts * kMaxTop];
+  Share share;
+  float group_max[kThreads];
+  double red0[kThreads / 32], red1[kThreads / 32];
+  float redb[kThreads / 32];
+  float cut;
+  uint32_t count;
+  uint32_t hist[256];
+  uint32_t digit, above;
+  uint32_t ties[kThreads / 32];
+};
+
+// The n largest of keys[0, c) (all different), in descending order, to out.
+// Every thread of the block takes part; barriers before and after are the
+// caller's. c^2 / 256 comparisons a thread: c is a few n, at most kKeyCap.
+__device__ __forceinline__ void rank_keys(const uint64_t* keys, int c, int n, uint64_t* out) {
+  for (int i = threadIdx.x; i < c; i += kThreads) {
+    const uint64_t k = keys[i];
+    int above = 0;
+    for (int j = 0; j < c; ++j) above += keys[j] > k ? 1 : 0;
+    if (above < n) out[above] = k;
+  }
+}
+
+// One thread's running sums against its base (a logit).
+struct Sums {
+  float s0, s1, base;
+};
+constexpr float kLowest = -3.402823466e+38f;  // the base before anything was seen
+
+__device__ __forceinline__ void rebase(Sums& s, float to, float c) {
+  const float by = (s.base - to) * c;  // 0 or less, -inf from kLowest
+  const float f = ex2(fmaxf(by, -200.f));
+  s.s1 = f == 0.f ? 0.f : fmaf(by, s.s0, s.s1) * f;
+  s.s0 *= f;
+  s.base = to;
+}
+
+__device__ __forceinline__ void add(Sums& s, float z, float c) {
+  const float x = fmaxf((z - s.base) * c, -200.f);
+  const float e = ex2(x);
+  s.s0 += e;
+  s.s1 = fmaf(e, x, s.s1);
+}
+
+__device__ __forceinline__ void keep(FwdSmem& sm, float z, uint32_t id) {
+  const uint32_t at = atomicAdd(&sm.count, 1u);
+  if (at < (uint32_t)kKeyCap) sm.keys[at] = token_key(z, id);
+}
+
+// An element on its own (a head, a tail, or one of a vector above the bound):
+// keep it where it is above `cut`, and move the base where it must.
+__device__ __forceinline__ void consider(FwdSmem& sm, Sums& s, float z, float c, uint32_t id,
+                                         float cut, bool or_equal) {
+  if (z > cut || (or_equal && z == cut && z > kNegInf)) keep(sm, z, id);
+  if ((z - s.base) * c > 64.f && z < INFINITY) rebase(s, z, c);
+}
+
+// The n largest of the stretch, digit by digit, for rows whose keys did not
+// fit: four histograms fix the n-th largest logit, then everything above it is
+// collected, and the ties at it in order of their ids.
+template <typename T>
+__device__ __noinline__ int search_again(FwdSmem& sm, const T* z, int len, uint32_t id0, int n) {
+  uint32_t prefix = 0, want = (uint32_t)n;
+  for (int shift = 24; shift >= 0; shift -= 8) {
+    __syncthreads();
+    sm.hist[threadIdx.x] = 0;
+    __syncthreads();
+    const uint32_t mask = shift == 24 ? 0u : 0xFFFFFFFFu << (shift + 8);
+    for (int i = threadIdx.x; i < (len + 31) / 32 * 32; i += kThreads) {
+      bool in = false;
+      uint32_t digit = 0;
+      if (i < len) {
+        const float v = to_f32(z[i]);
+        const uint32_t b = order_bits(v);
+        in = v > kNegInf && (b & mask) == (prefix & mask);
+        digit = (b >> shift) & 255u;
+      }
+      const uint32_t same = __match_any_sync(0xFFFFFFFFu, in ? digit : 256u);
+      if (in && (__ffs((int)same) - 1) == (int)(threadIdx.x & 31))
+        atomicAdd(&sm.hist[digit], (uint32_t)__popc(same));
+    }
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      uint32_t seen = 0;
+      int b = 255;
+      for (; b > 0; --b) {
+        if (seen + sm.hist[b] >= want) break;
+        seen += sm.hist[b];
+      }
+      sm.digit = (uint32_t)b;
+      sm.above = seen;
+    }
+    __syncthreads();
+    prefix |= sm.digit << shift;
+    want -= min(want, sm.above);
+  }
+  // prefix: the n-th largest logit (or less, where fewer are there); `want` ties
+  __syncthreads();
+  if (threadIdx.x == 0) sm.count = 0;
+  __syncthreads();
+  uint32_t ties = 0;
+  for (int i0 = 0; i0 < len; i0 += kThreads) {
+    const int i = i0 + (int)threadIdx.x;
+    bool tie = false;
+    float v = kNegInf;
+    if (i < len) {
+      v = to_f32(z[i]);
+      const uint32_t b = order_bits(v);
+      if (v > kNegInf && b > prefix) keep(sm, v, id0 + (uint32_t)i);
+      tie = v > kNegInf && b == prefix;
+    }
+    if (ties < want) {  // the same in every thread
+      const uint32_t ballot = __ballot_sync(0xFFFFFFFFu, tie);
+      if ((threadIdx.x & 31) == 0) sm.ties[threadIdx.x >> 5] = (uint32_t)__popc(ballot);
+      __syncthreads();
+      uint32_t before = ties, all = ties;
+      for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < (int)(threadIdx.x >> 5)) before += sm.ties[w];
+        all += sm.ties[w];
+      }
+      before += (uint32_t)__popc(ballot & ((1u << (threadIdx.x & 31)) - 1u));
+      if (tie && before < want) keep(sm, v, id0 + (uint32_t)i);
+      ties = all;
+      __syncthreads();
+    }
+  }
+  __syncthreads();
+  return (int)min(sm.count, (uint32_t)kKeyCap);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) forward_kernel(const FwdArgs a) {
+  __shared__ FwdSmem sm;
+  constexpr int kN = Vec<T>::kN;
+  const int parts = a.parts;
+  const int64_t row = (int64_t)blockIdx.x / parts;
+  const int part = (int)((int64_t)blockIdx.x - row * parts);
+  const int tid = threadIdx.x;
+  const int n = max(a.n, 1);  // the first alternative gives the maximum
+  const float tau = a.tau ? a.tau[row] : 1.f;
+  const bool tau_ok = tau > 0.f && tau < INFINITY;
+  const float c = exponent_scale(tau_ok ? tau : 1.f);
+
+  const int v0 = (int)min((int64_t)part * a.stretch, (int64_t)a.V);
+  const int len = min(a.stretch, a.V - v0);
+  const T* z = static_cast<const T*>(a.z) + row * a.ld + v0;
+  // [0, head): up to the first 16-byte boundary; [head, head + body kN): vectors
+  const int head = min((int)((16u - (uint32_t)(reinterpret_cast<uintptr_t>(z) & 15u)) % 16u) /
+                           (int)sizeof(T), len);
+  const int body = (len - head) / kN;
+  const int tail0 = head + body * kN;
+  const T* zb = z + head;
+
+  if (tid == 0) sm.count = 0;
+
+  Sums s{0.f, 0.f, kLowest};
+  float cut = kNegInf;   // nothing at or below it can be an alternative any more
+  float seen = kNegInf;  // only to catch NaN: the maximum of everything, NaN if any is
+  int groups = 32;       // group maxima for the first bound: at least n
+  while (groups < 4 * n && groups < kThreads) groups *= 2;
+  const int per_group = kThreads / groups;
+
+  bool bound = false;  // a finite bound has been found (the same in every thread)
+  int next_tighten = 4;
+  for (int it = 0, i0 = 0; i0 < body || it == 0; ++it, i0 += kThreads * kUnroll) {
+    Vec<T> v[kUnroll];
+    float vm[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int i = i0 + u * kThreads + tid;
+      if (i < body) v[u].load(zb + (int64_t)i * kN);
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int i = i0 + u * kThreads + tid;
+      vm[u] = i < body ? v[u].largest() : kNegInf;
+    }
+    bool equal = false;  // whether ties with the bound still count
+    if (!bound) {
+      float m = max_nan(max_nan(vm[0], vm[1]), max_nan(vm[2], vm[3]));
+      for (int o = 1; o < per_group; o *= 2) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+      if (tid % per_group == 0) sm.group_max[tid / per_group] = m;
+      if (tid == 0) sm.cut = kNegInf;
+      __syncthreads();
+      if (tid < groups) {  // the n-th largest group maximum (NaN and -inf count as least)
+        const float mine = sm.group_max[tid];
+        if (mine > kNegInf) {
+          int above = 0;
+          for (int j = 0; j < groups; ++j) {
+            const float o = sm.group_max[j];
+            above += (o > mine || (o == mine && j < tid)) ? 1 : 0;
+          }
+          if (above == n - 1) sm.cut = mine;
+          if (above == 0) sm.redb[0] = mine;
+        }
+      }
+      __syncthreads();
+      if (sm.cut > kNegInf) {
+        bound = true;
+        equal = true;  // the n elements of the bound are of this very chunk
+        cut = sm.cut;
+        const float to = fminf(sm.redb[0], 3.402823466e+38f);  // the base: the chunk's maximum
+        if (to > s.base) rebase(s, to, c);
+      }
+      __syncthreads();  // group_max, cut and redb are free again
+    } else if (it >= next_tighten && a.n > 1) {
+      next_tighten *= 4;
+      __syncthreads();
+      const int cnt = (int)min(sm.count, (uint32_t)kKeyCap);
+      const bool whole = sm.count <= (uint32_t)kKeyCap;
+      if (whole && cnt >= n) {
+        rank_keys(sm.keys, cnt, n, sm.top);
+        __syncthreads();
+        if (tid < n) sm.keys[tid] = sm.top[tid];
+        if (tid == 0) sm.count = (uint32_t)n;
+        cut = fmaxf(cut, key_logit(sm.top[n - 1]));
+      }
+      __syncthreads();
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int i = i0 + u * kThreads + tid;
+      if (i < body) {
+        float f[kN];
+        v[u].f32(f);
+        // also taken for NaN, and where no bound is known yet
+        if (!(vm[u] < cut) && (equal || !(vm[u] <= cut) || cut == kNegInf)) {
+          seen = max_nan(seen, vm[u]);
+          const uint32_t id = (uint32_t)(v0 + head + i * kN);
+#pragma unroll
+          for (int k = 0; k < kN; ++k) consider(sm, s, f[k], c, id + (uint32_t)k, cut, equal);
+        }
+#pragma unroll
+        for (int k = 0; k < kN; ++k) add(s, f[k], c);
+      }
+    }
+  }
+  // the elements outside the vectors: ids below (head) or above (tail) all others
+  for (int i = tid; i < head + (len - tail0); i += kThreads) {
+    const int at = i < head ? i : tail0 + (i - head);
+    const float f = to_f32(z[at]);
+    seen = max_nan(seen, f);
+    consider(sm, s, f, c, (uint32_t)(v0 + at), cut, true);
+    add(s, f, c);
+  }
+
+  // ---- join the block's sums (float64) and find its n largest
+  {
+    float top_base = s.base;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+      top_base = fmaxf(top_base, __shfl_xor_sync(0xFFFFFFFFu, top_base, o));
+    __syncthreads();
+    if ((tid & 31) == 0) sm.redb[tid >> 5] = top_base;
+    __syncthreads();
+    for (int w = 0; w < kThreads / 32; ++w) top_base = fmaxf(top_base, sm.redb[w]);
+    const double by = ((double)s.base - (double)top_base) * (double)c;
+    const double f = by < -300.0 ? 0.0 : exp2(by);
+    double s0 = (double)s.s0 * f;
+    double s1 = f == 0.0 ? 0.0 : ((double)s.s1 + by * (double)s.s0) * f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      s0 += __shfl_xor_sync(0xFFFFFFFFu, s0, o);
+      s1 += __shfl_xor_sync(0xFFFFFFFFu, s1, o);
+    }
+    if ((tid & 31) == 0) {
+      sm.red0[tid >> 5] = s0;
+      sm.red1[tid >> 5] = s1;
+    }
+    const int bad = __syncthreads_or(seen != seen || seen == INFINITY);
+    if (tid == 0) {
+      s0 = s1 = 0.0;
+      for (int w = 0; w < kThreads / 32; ++w) {
+        s0 += sm.red0[w];
+        s1 += sm.red1[w];
+      }
+      sm.share.s0 = s0;
+      sm.share.s1 = s1;
+      sm.share.base = top_base;
+      sm.share.bad = bad;
+    }
+  }
+  int cnt = (int)min(sm.count, (uint32_t)kKeyCap);
+  if (sm.count > (uint32_t)kKeyCap) {  // the same in every thread: a barrier has passed
+    cnt = search_again<T>(sm, z, len, (uint32_t)v0, n);
+  }
+  rank_keys(sm.keys, cnt, n, sm.top);
+  if (tid == 0) sm.share.found = min(cnt, n);
+
+  // ---- join the cluster's blocks
+  int found;
+  double s0, s1;
+  float base;
+  int bad;
+  const uint64_t* top = sm.top;
+  if (parts > 1) {
+    cg::cluster_group cluster = cg::this_cluster();
+    cluster.sync();
+    if (part == 0) {
+      for (int i = tid; i < parts * kMaxTop; i += kThreads) {
+        const int p = i / kMaxTop, j = i % kMaxTop;
+        const FwdSmem* other = cluster.map_shared_rank(&sm, p);
+        // absent ones get keys below every real one, all different
+        sm.joined[i] = j < other->share.found ? other->top[j] : (uint64_t)i;
+      }
+      base = kNegInf;
+      for (int p = 0; p < parts; ++p)
+        base = fmaxf(base, cluster.map_shared_rank(&sm, p)->share.base);
+      s0 = s1 = 0.0;
+      bad = 0;
+      found = 0;
+      for (int p = 0; p < parts; ++p) {
+        const Share sh = cluster.map_shared_rank(&sm, p)->share;
+        const double by = ((double)sh.base - (double)base) * (double)c;
+        const double f = by < -300.0 ? 0.0 : exp2(by);
+        s0 += sh.s0 * f;
+        s1 += f == 0.0 ? 0.0 : (sh.s1 + by * sh.s0) * f;
+        bad |= sh.bad;
+        found += sh.found;
+      }
+      found = min(found, n);
+    }
+    cluster.sync();  // the others' shared memory is no longer read
+    if (part != 0) return;
+    rank_keys(sm.joined, parts * kMaxTop, n, sm.top);
+    __syncthreads();
+  } else {
+    __syncthreads();
+    found = sm.share.found;
+    s0 = sm.share.s0;
+    s1 = sm.share.s1;
+    base = sm.share.base;
+    bad = sm.share.bad;
+  }
+
+  // ---- the row's results
+  int reason = (tau_ok ? 0 : STS_ROW_BAD_TEMPERATURE) | (bad ? STS_ROW_BAD_LOGIT : 0);
+  {
+    int out = 0;
+    for (int j = tid; j < a.m; j += kThreads) {
+      const int64_t y = a.tokens[row * a.tokens_ld + j];
+      out |= (y < -1 || y >= a.V) ? 1 : 0;
+    }
+    if (__syncthreads_or(out)) reason |= STS_ROW_BAD_TARGET;
+  }
+  const float nan = __int_as_float(0x7fc00000);
+  const bool empty = reason == 0 && found == 0;
+  const float zmax = found > 0 ? key_logit(top[0]) : kNegInf;
+  // S = sum 2^(c (z - zmax)); by: what the base is off zmax
+  const double by = found > 0 ? ((double)base - (double)zmax) * (double)c : 0.0;
+  const double total = s0 * exp2(by);
+  const double ln_total = log(total);
+  const float log_sum = reason ? nan : empty ? kNegInf : (float)ln_total;
+  if (tid == 0) {
+    if (a.logit_max) a.logit_max[row] = reason ? nan : zmax;
+    if (a.log_sum) a.log_sum[row] = log_sum;
+    if (a.lse)
+      a.lse[row] = reason ? nan : empty ? kNegInf : (float)((double)zmax / (double)tau + ln_total);
+    if (a.entropy) {
+      const double h = ln_total - kLn2 * (s1 / s0 + by);
+      a.entropy[row] = reason ? nan : empty ? 0.f : (float)fmax(h, 0.0);
+    }
+    if (a.flags)
+      a.flags[row] = reason ? (STS_ROW_INVALID | reason) : empty ? STS_ROW_EMPTY : 0;
+  }
+  const T* zrow = static_cast<const T*>(a.z) + row * a.ld;
+  for (int j = tid; j < a.m; j += kThreads) {
+    const int64_t y = a.tokens[row * a.tokens_ld + j];
+    float lp = nan;
+    if (!reason) {
+      if (y < 0)
+        lp = 0.f;
+      else if (empty)
+        lp = kNegInf;
+      else
+        lp = __fdiv_rn(to_f32(zrow[y]) - zmax, tau) - log_sum;
+    }
+    a.logprob[row * a.m + j] = lp;
+  }
+  for (int j = tid; j < a.n; j += kThreads) {
+    const bool has = !reason && j < found;
+    a.top_id[row * a.n + j] = has ? (int64_t)key_id(top[j]) : -1;
+    a.top_logprob[row * a.n + j] =
+        reason ? nan : has ? __fdiv_rn(key_logit(top[j]) - zmax, tau) - log_sum : kNegInf;
+  }
+}
+
+// ---------------------------------------------------------------- gradient
+
+struct BwdArgs {
+  const void* z;
+  int64_t ld;
+  int64_t T;
+  int V, parts, stretch;
+  const int64_t* tokens;
+  int64_t tokens_ld;
+  int m;
+  const float* tau;
+  int n;
+  const float *logit_max, *log_sum, *entropy;
+  const int32_t* flags;
+  const int64_t* top_id;
+  const float *grad, *grad_entropy, *grad_top;
+  void* out;
+  int64_t out_ld;
+};
+
+struct BwdSmem {
+  int64_t id[kMaxGiven + kMaxTop];
+  float g[kMaxGiven + kMaxTop];
+  float z[kMaxGiven + kMaxTop];
+  double part[kThreads / 32];
+};
+
+// kN results to p (kN output elements, 16-byte rows where kVecOut).
+template <typename O, int kN>
+__device__ __forceinline__ void store_vec(O* p, const float (&v)[kN]) {
+  union {
+    O o[kN];
+    uint4 w[(kN * sizeof(O) + 15) / 16];
+    uint2 h;
+  } u;
+#pragma unroll
+  for (int i = 0; i < kN; ++i) from_f32(v[i], u.o[i]);
+  if constexpr (kN * sizeof(O) == 8) {
+    *reinterpret_cast<uint2*>(p) = u.h;
+  } else {
+#pragma unroll
+    for (int i = 0; i < (int)(kN * sizeof(O) / 16); ++i) reinterpret_cast<uint4*>(p)[i] = u.w[i];
+  }
+}
+
+struct RowCoef {
+  float zmax, c, l2s;  // x = (z - zmax) c - l2s, p = 2^x
+  float a, b;          // dz = p (a + b x)
+};
+
+__device__ __forceinline__ float grad_of(float z, const RowCoef& k) {
+  const float x = fmaxf(fmaf(z - k.zmax, k.c, -k.l2s), -200.f);
+  return ex2(x) * fmaf(k.b, x, k.a);
+}
+
+template <typename T, typename O>
+__global__ void __launch_bounds__(kThreads) backward_kernel(const BwdArgs a) {
+  __shared__ BwdSmem sm;
+  constexpr int kN = Vec<T>::kN;
+  const int parts = a.parts;
+  const int64_t row = (int64_t)blockIdx.x / parts;
+  const int part = (int)((int64_t)blockIdx.x - row * parts);
+  const int tid = threadIdx.x;
+  const int v0 = (int)min((int64_t)part * a.stretch, (int64_t)a.V);
+  const int len = min(a.stretch, a.V - v0);
+  const T* zrow = static_cast<const T*>(a.z) + row * a.ld;
+  O* orow = static_cast<O*>(a.out) + row * a.out_ld;
+  const T* z = zrow + v0;
+  O* out = orow + v0;
+  const bool live = (a.flags[row] & (STS_ROW_INVALID | STS_ROW_EMPTY)) == 0;
+
+  // the tokens that get a share, with their logits: read before any block of
+  // the row writes, since the gradient may take the logits' place
+  const int count = (a.grad ? a.m : 0) + (a.grad_top ? a.n : 0);
+  const int given = a.grad ? a.m : 0;
+  double sum = 0.0;
+  if (live) {
+    for (int j = tid; j < count; j += kThreads) {
+      int64_t id;
+      float g;
+      if (j < given) {
+        id = a.tokens[row * a.tokens_ld + j];
+        g = a.grad[row * a.m + j];
+      } else {
+        id = a.top_id[row * a.n + (j - given)];
+        g = a.grad_top[row * a.n + (j - given)];
+      }
+      float zv = kNegInf;
+      if (id >= 0 && id < a.V) zv = to_f32(zrow[id]);
+      const bool valid = zv > kNegInf;
+      sm.id[j] = valid ? id : -1;
+      sm.g[j] = g;
+      sm.z[j] = zv;
+      if (valid) sum += (double)g;
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+  if ((tid & 31) == 0) sm.part[tid >> 5] = sum;
+  if (parts > 1)
+    cg::this_cluster().sync();
+  else
+    __syncthreads();
+  sum = 0.0;
+  for (int w = 0; w < kThreads / 32; ++w) sum += sm.part[w];
+
+  RowCoef k{0.f, 0.f, 0.f, 0.f, 0.f};
+  float tau = 1.f;
+  if (live) {
+    tau = a.tau ? a.tau[row] : 1.f;
+    const double h = a.grad_entropy ? (double)a.grad_entropy[row] : 0.0;
+    k.zmax = a.logit_max[row];
+    k.c = exponent_scale(tau);
+    k.l2s = (float)((double)a.log_sum[row] * kLog2eD);
+    k.a = (float)(-(sum + (h != 0.0 ? h * (double)a.entropy[row] : 0.0)) / (double)tau);
+    k.b = (float)(-h * kLn2 / (double)tau);
+  }
+
+  const int head = min((int)((16u - (uint32_t)(reinterpret_cast<uintptr_t>(z) & 15u)) % 16u) /
+                           (int)sizeof(T), len);
+  const int body = (len - head) / kN;
+  const int tail0 = head + body * kN;
+  const T* zb = z + head;
+  O* ob = out + head;
+  constexpr uintptr_t kOutAlign = kN * sizeof(O) >= 16 ? 15u : 7u;
+  const bool vec_out = (reinterpret_cast<uintptr_t>(ob) & kOutAlign) == 0;
+
+  for (int i0 = 0; i0 < body; i0 += kThreads * kUnroll) {
+    Vec<T> v[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int i = i0 + u * kThreads + tid;
+      // not __ldg: the output may be the logits themselves
+      if (live && i < body) v[u].w = *reinterpret_cast<const uint4*>(zb + (int64_t)i * kN);
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int i = i0 + u * kThreads + tid;
+      if (i < body) {
+        float f[kN];
+        if (live) {
+          v[u].f32(f);
+#pragma unroll
+          for (int j = 0; j < kN; ++j) f[j] = grad_of(f[j], k);
+        } else {
+#pragma unroll
+          for (int j = 0; j < kN; ++j) f[j] = 0.f;
+        }
+        O* p = ob + (int64_t)i * kN;
+        if (vec_out) {
+          store_vec<O, kN>(p, f);
+        } else {
+#pragma unroll
+          for (int j = 0; j < kN; ++j) from_f32(f[j], p[j]);
+        }
+      }
+    }
+  }
+  for (int i = tid; i < head + (len - tail0); i += kThreads) {
+    const int at = i < head ? i : tail0 + (i - head);
+    from_f32(live ? grad_of(to_f32(z[at]), k) : 0.f, out[at]);
+  }
+  if (!live || count == 0) return;
+  __syncthreads();  // the tokens' own elements are written again, whole, by their first mention
+  for (int j = tid; j < count; j += kThreads) {
+    const int64_t id = sm.id[j];
+    if (id < v0 || id >= (int64_t)v0 + len) continue;
+    double g = 0.0;
+    bool first = true;
+    for (int i = 0; i < count; ++i) {
+      if (sm.id[i] != id) continue;
+      if (i < j) {
+        first = false;
+        break;
+      }
+      g += (double)sm.g[i];
+    }
+    if (first) from_f32((float)(g / (double)tau + (double)grad_of(sm.z[j], k)), orow[id]);
+  }
+}
+
+// ---------------------------------------------------------------- launches
+
+// Parts per row: as many as it takes to give every SM `want` blocks, at most 8,
+// and none shorter than one round of the loop.
+int parts_for(int64_t T, int64_t V, int elem, int sms) {
+  const int64_t round = (int64_t)kThreads * kUnroll * (16 / elem);
+  int parts = 1;
+  while (parts < kMaxParts && T * parts < (int64_t)sms * 4 && V > round * parts) parts *= 2;
+  return parts;
+}
+
+template <typename K, typename A>
+cudaError_t launch_rows(K kernel, const A& a, cudaStream_t st) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(a.T * a.parts));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)a.parts;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = a.parts > 1 ? 1 : 0;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, a);
+  const cudaError_t last = cudaGetLastError();
+  return e != cudaSuccess ? e : last;
+}
+
+int elem_size(int dtype) {
+  return dtype == STS_DTYPE_F32 ? 4 : dtype == STS_DTYPE_BF16 || dtype == STS_DTYPE_F16 ? 2 : 0;
+}
+
+constexpr int64_t kMost = (int64_t(1) << 31) - 1;
+
+// Host checks shared by both directions; *done where there is nothing to do.
+sts_status check_token_rows(const sts_token_rows* r, bool* done) {
+  *done = false;
+  if (!r) return STS_ERR_NULL;
+  const int es = elem_size(r->dtype);
+  if (!es) return STS_ERR_DTYPE;
+  if (r->T < 0 || r->T > kMost / kMaxParts || r->V < 1 || r->V > kMost - 1024) return STS_ERR_SHAPE;
+  if (r->m < 0 || r->m > kMaxGiven || r->top_n < 0 || r->top_n > kMaxTop) return STS_ERR_SHAPE;
+  if (r->T > 1 && (r->ld < r->V || r->tokens_ld < r->m)) return STS_ERR_SHAPE;
+  if (r->T == 0) {
+    *done = true;
+    return STS_OK;
+  }
+  if (!r->logits || (r->m > 0 && !r->tokens)) return STS_ERR_NULL;
+  if ((reinterpret_cast<uintptr_t>(r->logits) % (unsigned)es) != 0) return STS_ERR_SHAPE;
+  return STS_OK;
+}
+
+}  // namespace
+}  // namespace sts
+
+using namespace sts;
+
+extern "C" sts_status sts_token_logprobs(const sts_token_rows* rows, float* logprob,
+                                         const sts_token_stats* stats, sts_stream_t stream) {
+  bool done = false;
+  const sts_status cs = check_token_rows(rows, &done);
+  if (cs != STS_OK || done) return cs;
+  if (!stats || (rows->m > 0 && !logprob)) return STS_ERR_NULL;
+  if (rows->top_n > 0 && (!stats->top_id || !stats->top_logprob)) return STS_ERR_NULL;
+  int sms = 0;
+  const sts_status ds = current_device(&sms);
+  if (ds != STS_OK) return ds;
+  FwdArgs a{};
+  a.z = rows->logits;
+  a.ld = rows->ld;
+  a.T = rows->T;
+  a.V = (int)rows->V;
+  a.parts = parts_for(rows->T, rows->V, elem_size(rows->dtype), sms);
+  a.stretch = (int)(((rows->V + a.parts - 1) / a.parts + 63) / 64 * 64);
+  a.tokens = rows->tokens;
+  a.tokens_ld = rows->tokens_ld;
+  a.m = (int)rows->m;
+  a.tau = rows->temperature;
+  a.n = (int)rows->top_n;
+  a.logprob = logprob;
+  a.logit_max = stats->logit_max;
+  a.log_sum = stats->log_sum;
+  a.lse = stats->lse;
+  a.entropy = stats->entropy;
+  a.flags = stats->flags;
+  a.top_id = stats->top_id;
+  a.top_logprob = stats->top_logprob;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const LaunchMark mark = launch_begin(STS_KERNEL_TOKEN_LOGPROBS, st);
+  const cudaError_t e = rows->dtype == STS_DTYPE_F32    ? launch_rows(forward_kernel<float>, a, st)
+                        : rows->dtype == STS_DTYPE_BF16 ? launch_rows(forward_kernel<__nv_bfloat16>, a, st)
+                                                        : launch_rows(forward_kernel<__half>, a, st);
+  launch_end(mark, st);
+  return e == cudaSuccess ? STS_OK : STS_ERR_CUDA;
+}
+
+namespace sts {
+namespace {
+
+template <typename T>
+cudaError_t launch_backward(const BwdArgs& a, int out_dtype, cudaStream_t st) {
+  return out_dtype == STS_DTYPE_F32    ? launch_rows(backward_kernel<T, float>, a, st)
+         : out_dtype == STS_DTYPE_BF16 ? launch_rows(backward_kernel<T, __nv_bfloat16>, a, st)
+                                       : launch_rows(backward_kernel<T, __half>, a, st);
+}
+
+}  // namespace
+}  // namespace sts
+
+extern "C" sts_status sts_token_logprobs_backward(const sts_token_rows* rows,
+                                                  const sts_token_stats* saved,
+                                                  const float* grad_logprob,
+                                                  const float* grad_entropy, const float* grad_top,
+                                                  void* dlogits, int dlogits_dtype,
+                                                  int64_t dlogits_ld, sts_stream_t stream) {
+  const int os = elem_size(dlogits_dtype);
+  if (!os) return STS_ERR_DTYPE;
+  bool done = false;
+  const sts_status cs = check_token_rows(rows, &done);
+  if (cs != STS_OK) return cs;
+  if (rows->T > 1 && dlogits_ld < rows->V) return STS_ERR_SHAPE;
+  if (done) return STS_OK;
+  if (!saved || !saved->logit_max || !saved->log_sum || !saved->flags || !dlogits)
+    return STS_ERR_NULL;
+  if (grad_entropy && !saved->entropy) return STS_ERR_NULL;
+  if (grad_top && rows->top_n > 0 && !saved->top_id) return STS_ERR_NULL;
+  if ((reinterpret_cast<uintptr_t>(dlogits) % (unsigned)os) != 0) return STS_ERR_SHAPE;
+  // the gradient may take the logits' own place, and no other part of them
+  const int es = elem_size(rows->dtype);
+  const uintptr_t z0 = reinterpret_cast<uintptr_t>(rows->logits);
+  const uintptr_t o0 = reinterpret_cast<uintptr_t>(dlogits);
+  const uintptr_t z1 = z0 + (uintptr_t)(((rows->T - 1) * (rows->T > 1 ? rows->ld : 0) + rows->V) * es);
+  const uintptr_t o1 = o0 + (uintptr_t)(((rows->T - 1) * (rows->T > 1 ? dlogits_ld : 0) + rows->V) * os);
+  if (z0 < o1 && o0 < z1 &&
+      !(z0 == o0 && rows->dtype == dlogits_dtype && (rows->T == 1 || rows->ld == dlogits_ld)))
+    return STS_ERR_SHAPE;
+  int sms = 0;
+  const sts_status ds = current_device(&sms);
+  if (ds != STS_OK) return ds;
+  BwdArgs a{};
+  a.z = rows->logits;
+  a.ld = rows->ld;
+  a.T = rows->T;
+  a.V = (int)rows->V;
+  a.parts = parts_for(rows->T, rows->V, es, sms);
+  a.stretch = (int)(((rows->V + a.parts - 1) / a.parts + 63) / 64 * 64);
+  a.tokens = rows->tokens;
+  a.tokens_ld = rows->tokens_ld;
+  a.m = (int)rows->m;
+  a.tau = rows->temperature;
+  a.n = (int)rows->top_n;
+  a.logit_max = saved->logit_max;
+  a.log_sum = saved->log_sum;
+  a.entropy = saved->entropy;
+  a.flags = saved->flags;
+  a.top_id = saved->top_id;
+  a.grad = rows->m > 0 ? grad_logprob : nullptr;
+  a.grad_entropy = grad_entropy;
+  a.grad_top = rows->top_n > 0 ? grad_top : nullptr;
+  a.out = dlogits;
+  a.out_ld = dlogits_ld;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const LaunchMark mark = launch_begin(STS_KERNEL_TOKEN_GRAD, st);
+  const cudaError_t e = rows->dtype == STS_DTYPE_F32 ? launch_backward<float>(a, dlogits_dtype, st)
+                        : rows->dtype == STS_DTYPE_BF16
+                            ? launch_backward<__nv_bfloat16>(a, dlogits_dtype, st)
+                            : launch_backward<__half>(a, dlogits_dtype, st);
+  launch_end(mark, st);
+  return e == cudaSuccess ? STS_OK : STS_ERR_CUDA;
+}

@@ -129,22 +129,9 @@ TimingState g_timing;
 // two events around it on the launch stream.
 template <typename F>
 cudaError_t timed_launch(int kind, cudaStream_t st, F&& launch) {
-  g_launches[kind].fetch_add(1, std::memory_order_relaxed);
-  cudaEvent_t b = nullptr, e = nullptr;
-  {
-    std::lock_guard<std::mutex> lock(g_timing.mu);
-    if (g_timing.on) {
-      b = g_timing.get();
-      e = g_timing.get();
-    }
-  }
-  if (b) cudaEventRecord(b, st);
+  const LaunchMark mark = launch_begin(kind, st);
   const cudaError_t err = launch();
-  if (e) {
-    cudaEventRecord(e, st);
-    std::lock_guard<std::mutex> lock(g_timing.mu);
-    g_timing.recs.push_back({kind, b, e});
-  }
+  launch_end(mark, st);
   return err;
 }
 
@@ -482,6 +469,40 @@ sts_status backward_impl(const sts_shape* shape, const void* H, const void* W,
 }
 
 }  // namespace
+
+LaunchMark launch_begin(int kind, cudaStream_t st) {
+  g_launches[kind].fetch_add(1, std::memory_order_relaxed);
+  LaunchMark mark{kind, nullptr, nullptr};
+  {
+    std::lock_guard<std::mutex> lock(g_timing.mu);
+    if (g_timing.on) {
+      mark.begin = g_timing.get();
+      mark.end = g_timing.get();
+    }
+  }
+  if (mark.begin) cudaEventRecord(mark.begin, st);
+  return mark;
+}
+
+void launch_end(const LaunchMark& mark, cudaStream_t st) {
+  if (!mark.end) return;
+  cudaEventRecord(mark.end, st);
+  std::lock_guard<std::mutex> lock(g_timing.mu);
+  g_timing.recs.push_back({mark.kind, mark.begin, mark.end});
+}
+
+sts_status current_device(int* sms) {
+  DeviceInfo info;
+  const sts_status s = device_info(info);
+  if (s == STS_OK) *sms = info.sms;
+  return s;
+}
+
+bool tensor_map_2d(CUtensorMap* m, const void* base, CUtensorMapDataType dt, uint64_t inner,
+                   uint64_t outer, uint64_t stride_bytes, uint32_t box_inner, uint32_t box_outer) {
+  return map2d(m, base, dt, inner, outer, stride_bytes, box_inner, box_outer);
+}
+
 }  // namespace sts
 
 using namespace sts;
@@ -495,7 +516,7 @@ const char* sts_status_string(sts_status s) {
     case STS_OK: return "ok";
     case STS_ERR_NULL: return "a required pointer is NULL";
     case STS_ERR_SHAPE: return "invalid shape, alignment or metadata length";
-    case STS_ERR_DTYPE: return "operands must be bf16 (fp8 heads are not supported)";
+    case STS_ERR_DTYPE: return "an operand has a dtype this entry point does not take (sts_forward: bf16 only)";
     case STS_ERR_TEMPERATURE: return "temperature must be finite and > 0";
     case STS_ERR_TOP_K: return "invalid top_k";
     case STS_ERR_TOP_P: return "top_p must be in (0, 1]";

@@ -30,6 +30,24 @@ static_assert(sizeof(WsHeader) == 256, "workspace header is 256 bytes");
 constexpr size_t kAlign = 1024;
 __host__ __device__ inline size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 
+// Every kernel launch of the library is counted, and timed while timing is on
+// (sts_timing_enable): launch_begin before it, launch_end after it, both on the
+// launch stream.
+struct LaunchMark {
+  int kind;
+  cudaEvent_t begin, end;  // null while timing is off
+};
+LaunchMark launch_begin(int kind, cudaStream_t st);
+void launch_end(const LaunchMark& mark, cudaStream_t st);
+
+// The current device's SM count; an error where it is not sm_100.
+sts_status current_device(int* sms);
+
+// A tensor map of a row-major matrix [outer][inner] with rows
+// stride_bytes apart, read in boxes of box_outer rows x 128 bytes, 128-byte swizzle. False on failure.
+bool tensor_map_2d(CUtensorMap* m, const void* base, CUtensorMapDataType dt, uint64_t inner,
+                   uint64_t outer, uint64_t stride_bytes, uint32_t box_inner, uint32_t box_outer);
+
 // Resolver modes.
 enum ResolveMode : int { kModeForward = 0, kModeSample = 1, kModeFilter = 2 };
 
