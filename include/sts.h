@@ -367,8 +367,9 @@ typedef enum {
  * smaller), x ~ q * scale:
  *   scale = a / top, a the largest finite |x| of the block, top the largest
  *           code (448 for e4m3, 57344 for e5m2); 1 where that quotient is 0
- *   q     = x / scale (IEEE fp32 division), limited to +-top, rounded to
- *           nearest even; NaN where x is not finite
+ *   q     = x (1 / scale) (reciprocal and product rounded to fp32; x / scale
+ *           where scale < 2^-126), limited to +-top, rounded to nearest even;
+ *           NaN where x is not finite
  * x_dtype: STS_DTYPE_F32, _BF16 or _F16; element (r, k) at x[r * stride_r + k *
  * stride_k], one of the strides 1 (a transposed view has stride_r == 1), the
  * other at least the extent it steps over. q_dtype: STS_DTYPE_E4M3 or _E5M2;

@@ -990,10 +990,9 @@ def sts_token_logprobs(logits, tokens=None, *, temperature=None, top_n=0, entrop
 
     ``tokens`` int64 [T] or [T, m] (m <= 512, -1: no token); ``temperature`` fp32 [T] (default 1).
     Returns ``(logprob, saved)``: logprob fp32 of tokens' shape (None without tokens), and a dict of
-    ``lse``, ``logit_max``, ``log_sum`` [T] fp32, ``flags`` [T] int32, with ``entropy`` also
-    ``entropy`` [T] (nats), with ``top_n`` (<= 64) also ``top_id`` [T, top_n] int64 and
-    ``top_logprob`` [T, top_n]: the most probable tokens, ties by the lower id, -1 and -inf where
-    fewer are unmasked. Invalid rows give NaN and -1 (``flags``); with ``check`` the call
+    ``lse``, ``logit_max``, ``log_sum`` [T] fp32, ``flags`` [T] int32, ``top_id`` [T, top_n] int64
+    and ``top_logprob`` [T, top_n] (``top_n`` <= 64: the most probable tokens, ties by the lower
+    id, -1 and -inf where fewer are unmasked), with ``entropy`` also ``entropy`` [T] (nats). Invalid rows give NaN and -1 (``flags``); with ``check`` the call
     synchronises and raises on them."""
     lib = load()
     rows = _token_rows(logits, tokens, temperature, top_n)
@@ -1007,12 +1006,11 @@ def sts_token_logprobs(logits, tokens=None, *, temperature=None, top_n=0, entrop
         saved = {"lse": stats[0], "logit_max": stats[1], "log_sum": stats[2], "flags": flags}
         if entropy:
             saved["entropy"] = stats[3]
-        logprob = top_id = top_logprob = None
+        logprob = None
         if tokens is not None:
             logprob = torch.empty(tokens.shape, dtype=_F32, device=dev)
-        if n:
-            saved["top_id"] = top_id = torch.empty((T, n), dtype=torch.int64, device=dev)
-            saved["top_logprob"] = top_logprob = torch.empty((T, n), dtype=_F32, device=dev)
+        saved["top_id"] = top_id = torch.empty((T, n), dtype=torch.int64, device=dev)
+        saved["top_logprob"] = top_logprob = torch.empty((T, n), dtype=_F32, device=dev)
         out = _TokenStats(_at(stats[1]), _at(stats[2]), _at(stats[0]),
                           _at(stats[3]) if entropy else None, _at(flags), _at(top_id),
                           _at(top_logprob))

@@ -6,30 +6,38 @@
 // with b[n, kb] per row, or shared by 128 rows; then / tau_m, + C.
 //
 // The inner sums run on the tensor cores (tcgen05 kind::f8f6f4, fp32
-// accumulators in tensor memory); scales differ from block to block, so each
+// accumulators in tensor memory). Scales differ from block to block, so each
 // block's 128 x NT products leave tensor memory once and are scaled and summed
-// in fp32 registers. That takes NT / 2 FMAs a thread and block beside the
-// tensor cores' 2 NT clocks, so it hides behind them as long as both have
-// accumulators to work on: 2 (NT = 256) or 4 of them alternate.
+// in fp32 registers, beside the tensor cores' 2 NT clocks for the block. A
+// thread's row is a lane of tensor memory, so a scale that belongs to the rows
+// is one register, while one that differs from column to column has to be
+// broadcast from shared memory at one column a clock for the whole SM. Hence
+// two forms of the kernel:
+//   wide    (M > 128) A's rows are the 128 lanes, B's rows the 256 columns. With
+//           b shared by 128 rows a block costs a thread 64 packed FMAs and no
+//           broadcast. With b per row the 4 x 256 broadcasts (1,024 clocks) are
+//           what bounds it. C leaves through swizzled shared memory by TMA.
+//   narrow  (M <= 128) B's rows are the lanes, A's rows the NT = 16 .. 128
+//           columns: it streams B once, bound by HBM, and the broadcasts (4 NT
+//           clocks a block) hide behind that. The 32 lanes of a warp write
+//           consecutive elements of C. A tile has as many rows of B (at most
+//           128) as gives every SM the same share of them.
 //
-// B's rows (a head's vocabulary) are the 128 rows of the tensor core's tile and
-// A's rows (tokens) its NT columns, NT = 16 .. 256:
-//   - a few tokens take a narrow tile, and then the kernel only streams B;
-//   - a thread owns one n and NT / 2 rows m of C, so the 32 lanes of a warp
-//     write 128 (fp32) consecutive bytes of C and need no staging;
-//   - b[n, kb] is a register, a[m, kb] a broadcast from shared memory, whatever
-//     the strides of the scales are (4-byte asynchronous copies bring them).
-//
-// One CTA per SM, 320 threads:
-//   warp 0      producer: TMA loads of B 128 x 128 and A NT x 128 bytes into a
-//               ring (128-byte swizzle), and the block's scales into a second
-//   warp 1      one thread issues 4 tcgen05.mma (K = 32 each) per block
-//   warps 2..9  scale and sum; warp w reads tensor memory lanes 32 (w % 4)..
-//               and one half of the columns
+// One CTA per SM, 384 threads:
+//   warp 0       TMA loads of both operands into a ring of stages of 128 bytes
+//                of k (128-byte swizzle)
+//   warp 1       one thread issues 4 tcgen05.mma (K = 32 each) per block into
+//                one of 2 (wide) or 4 accumulators
+//   warp 2       the blocks' scales, into a ring of their own (4-byte
+//                asynchronous copies: any strides)
+//   warps 4..11  scale and sum; warp w reads lanes 32 (w % 4).. and one half of
+//                the columns
 // Tiles are walked persistently, 16 tiles of A's rows for one of B's, so that
-// B is read from L2. Where there are too few tiles for the SMs, a cluster of 2,
-// 4 or 8 CTAs shares a tile: each takes a stretch of k, the sums meet in
-// distributed shared memory and are added in the order of k.
+// operands are read from L2. Where there are too few tiles for the SMs, a
+// cluster of 2, 4 or 8 CTAs shares a tile: each takes a stretch of k, the sums
+// meet in distributed shared memory and are added in the order of k.
+#include <cstring>
+
 #include <cooperative_groups.h>
 
 #include "sts_device.cuh"
@@ -39,90 +47,122 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 320;
+constexpr int kThreads = 384;
 constexpr int kSumWarps = 8;
-constexpr int kRowsB = 128;
+constexpr int kLanes = 128;  // rows of the tensor core's tile
 constexpr int kBlock = 128;  // k per scale, and bytes per row of a stage
 constexpr int kGroup = 16;   // tiles of A's rows per raster group
-constexpr int kScaleSlots = 8;
 constexpr int kMaxSplit = 8;
+constexpr int kStaging = 2048;  // one of a warp's two staging buffers: 32 rows x 64 bytes
 
-template <int NT>
+// kUniform: the columns' scales are shared by 128 of them (wide, b shared).
+template <int NT, bool kWide, bool kUniform>
 struct Shape {
-  static constexpr int kBufs = NT == 256 ? 2 : 4;
+  static_assert(!kUniform || kWide, "a uniform column scale is the wide form's");
+  static constexpr int kBufs = NT >= 128 ? 2 : 4;
   static constexpr uint32_t kTmemCols = NT * kBufs;
-  static constexpr uint32_t kBytesB = kRowsB * kBlock;
-  static constexpr uint32_t kBytesA = NT * kBlock;
-  static constexpr uint32_t kStage = kBytesB + kBytesA;
-  static constexpr int kStages = (int)(196608u / kStage) < 10 ? (int)(196608u / kStage) : 10;
-  static constexpr uint32_t kSlot = (NT + kRowsB) * 4;
-  static constexpr size_t kSmem = 1024 + (size_t)kStages * kStage + kScaleSlots * kSlot + 512;
+  static constexpr uint32_t kLaneBytes = kLanes * kBlock;
+  static constexpr uint32_t kColBytes = NT * kBlock;
+  static constexpr uint32_t kStage = kLaneBytes + kColBytes;
+  static constexpr int kStages = kWide ? (kUniform ? 4 : 3) : (NT == 128 ? 6 : 8);
+  // stages and accumulators repeat together after this many blocks
+  static constexpr int kTurn = kStages % kBufs == 0 ? kStages : kStages * kBufs;
+  static constexpr int kSlots = kWide ? 4 : 8;
+  static constexpr int kColScales = kUniform ? 4 : NT;  // floats of a slot beyond the lanes' 128
+  static constexpr uint32_t kSlot = (kLanes + kColScales) * 4;
+  static constexpr uint32_t kStagingBytes = kWide ? kSumWarps * 2 * kStaging : 0;
+  static constexpr int kBars = 2 * kStages + 2 * kSlots + 2 * kBufs + 1;
+  static constexpr size_t kSmem = (size_t)kStages * kStage + kStagingBytes + kSlots * kSlot + kBars * 8 + 16;
+  static constexpr int kPitch = NT + 1;  // floats between rows of a split's sums
   static_assert(kSmem <= 227 * 1024, "shared memory of one CTA");
-  static_assert((size_t)kStages * kStage >= (size_t)kRowsB * NT * 4, "a split's sums fit the ring");
+  static_assert((size_t)kStages * kStage >= (size_t)kLanes * kPitch * 4, "a split's sums fit the ring");
 };
 
 struct ProductArgs {
-  int M, N, K, kb;  // kb: blocks along k
-  int tiles_m, tiles_n;
-  const float* a_scale;
-  int64_t a_sr, a_sk;
-  const float* b_scale;
-  int64_t b_sr, b_sk;
-  int b_shared;  // 1: one scale per 128 rows of B
+  int M, N, kb;         // kb: blocks along k
+  int lane_n, col_n;    // rows of the two operands (lanes: A if wide, else B)
+  int height;           // rows of the lanes' operand per tile (128 if wide)
+  int tiles_l, tiles_c;
+  const float* lane_scale;
+  int64_t lane_sr, lane_sk;
+  int lane_shift;       // row >> lane_shift is the row of its scale
+  const float* col_scale;
+  int64_t col_sr, col_sk;
   uint32_t idesc;
   const float* tau;
   void* C;
   int64_t ldc;
   int accumulate;
-  int split;  // CTAs per tile (cluster size)
+  int split;            // CTAs per tile (cluster size)
+  int tma_out;          // C can be written by TMA (wide)
   int* err;
 };
 
-// D[tmem] (+)= A[smem] . B[smem]^T, 8-bit inputs, fp32 accumulate, one CTA.
-__device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
-                                        uint32_t idesc, uint32_t accumulate) {
+// The issuing helpers below take `mine`: every lane of the warp calls them, so
+// that control flow and operands stay uniform, and the elected lane acts.
+__device__ __forceinline__ uint32_t elected() {
+  uint32_t e;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "elect.sync _|p, 0xFFFFFFFF;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(e));
+  return e;
+}
+
+// D[tmem] (+)= A[smem] . B[smem]^T over a block of 128 bytes of k: four MMAs of
+// 8-bit inputs, fp32 accumulate, one CTA; the first overwrites D. A
+// descriptor's low bits are the address in units of 16 bytes.
+__device__ __forceinline__ void umma_block(uint32_t mine, uint32_t d_tmem, uint64_t a_desc,
+                                           uint64_t b_desc, uint32_t idesc) {
+  asm volatile(
+      "{\n\t.reg .pred q, no, yes;\n\t.reg .b64 a1, b1, a2, b2, a3, b3;\n\t"
+      "setp.ne.b32 q, %4, 0;\n\t"
+      "setp.ne.b32 no, 0, 0;\n\t"
+      "setp.eq.b32 yes, 0, 0;\n\t"
+      "add.u64 a1, %1, 2;\n\tadd.u64 b1, %2, 2;\n\t"
+      "add.u64 a2, %1, 4;\n\tadd.u64 b2, %2, 4;\n\t"
+      "add.u64 a3, %1, 6;\n\tadd.u64 b3, %2, 6;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, no;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a1, b1, %3, yes;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a2, b2, %3, yes;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a3, b3, %3, yes;\n\t}\n" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(mine)
+      : "memory");
+}
+
+// Arrives on `bar` when every tcgen05 op issued so far by the elected lane is done.
+__device__ __forceinline__ void commit(uint32_t mine, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n" ::"r"(bar),
+      "r"(mine)
+      : "memory");
+}
+
+// Two boxes into shared memory; `bar` counts their bytes.
+__device__ __forceinline__ void load_stage(uint32_t mine, uint32_t bar, uint32_t bytes,
+                                           uint32_t dst_l, const CUtensorMap* map_l, int32_t y_l,
+                                           uint32_t dst_c, const CUtensorMap* map_c, int32_t y_c,
+                                           int32_t x) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %9, 0;\n\t"
+      "@q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t"
+      "@q cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%2], [%3, {%8, %4}], [%0];\n\t"
+      "@q cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%5], [%6, {%8, %7}], [%0];\n\t}\n" ::"r"(bar),
+      "r"(bytes), "r"(dst_l), "l"(reinterpret_cast<uint64_t>(map_l)), "r"(y_l), "r"(dst_c),
+      "l"(reinterpret_cast<uint64_t>(map_c)), "r"(y_c), "r"(x), "r"(mine)
       : "memory");
 }
 
 // Instruction descriptor, kind::f8f6f4: fp32 accumulator (bits 4-5 = 1), the
-// formats of the 128-row operand in bits 7-9 and of the other in bits 10-12
+// formats of the lanes' operand in bits 7-9 and of the columns' in bits 10-12
 // (0 e4m3, 1 e5m2), both K-major, N >> 3 in bits 17-22, M >> 4 in bits 24-28.
 uint32_t idesc_f8(bool rows_e5, bool cols_e5, int M, int N) {
   return (1u << 4) | ((rows_e5 ? 1u : 0u) << 7) | ((cols_e5 ? 1u : 0u) << 10) |
          ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
-}
-
-__device__ __forceinline__ void tmem_ld_x8(uint32_t taddr, uint32_t* r) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7])
-      : "r"(taddr));
-}
-
-__device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t* r) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
-      "%12, %13, %14, %15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr));
-}
-
-template <int N>
-__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[N]) {
-  if constexpr (N == 8)
-    tmem_ld_x8(taddr, r);
-  else if constexpr (N == 16)
-    tmem_ld_x16(taddr, r);
-  else
-    tmem_ld_32x32b_x32(taddr, r);
 }
 
 // 4 bytes global -> shared, or 4 zero bytes where !live (src is not read then).
@@ -138,49 +178,157 @@ __device__ __forceinline__ void copies_arrive(uint32_t bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
-__device__ __forceinline__ void tile_coords(int t, int tiles_m, int tiles_n, int& tm, int& tn) {
-  const int64_t per = (int64_t)kGroup * tiles_n;
+
+// 32 lanes x kN consecutive columns of tensor memory; complete after tmem_wait.
+template <int kN>
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[kN]) {
+  static_assert(kN == 8 || kN == 16 || kN == 32, "");
+  if constexpr (kN == 32) {
+    tmem_ld_32x32b_x32(taddr, r);
+  } else if constexpr (kN == 8) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+                   "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+  } else {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+        "%11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+  }
+}
+
+// Waits for this thread's loads from tensor memory; the registers pass through,
+// so that nothing that uses them moves above the wait.
+template <int kN>
+__device__ __forceinline__ void tmem_wait(uint32_t (&r)[kN]) {
+  if constexpr (kN == 32) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 32; i += 8)
+      asm volatile("" : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]),
+                   "+r"(r[i + 5]), "+r"(r[i + 6]), "+r"(r[i + 7]));
+  } else if constexpr (kN == 8) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                   "+r"(r[6]), "+r"(r[7])::"memory");
+  } else {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                   "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                   "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
+  }
+}
+
+// Two fp32 in one register pair; one instruction for both, rounded each.
+__device__ __forceinline__ uint64_t pair(float x, float y) {
+  uint64_t p;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(x), "f"(y));
+  return p;
+}
+__device__ __forceinline__ uint64_t pair(uint32_t x, uint32_t y) {
+  uint64_t p;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "r"(x), "r"(y));
+  return p;
+}
+__device__ __forceinline__ float2 unpair(uint64_t p) {
+  float2 v;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
+// Whether the phase has completed, without waiting.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+// Tile t: groups of kGroup tiles of A's rows, all of B's tiles within a group.
+template <bool kWide>
+__device__ __forceinline__ void tile_coords(const ProductArgs& p, int t, int& tl, int& tc) {
+  const int na = kWide ? p.tiles_l : p.tiles_c, nb = kWide ? p.tiles_c : p.tiles_l;
+  const int64_t per = (int64_t)kGroup * nb;
   const int g = (int)(t / per);
   const int first = g * kGroup;
-  const int gm = min(kGroup, tiles_m - first);
+  const int ga = min(kGroup, na - first);
   const int r = (int)(t - g * per);
-  tm = first + r % gm;
-  tn = r / gm;
+  const int ta = first + r % ga, tb = r / ga;
+  tl = kWide ? ta : tb;
+  tc = kWide ? tb : ta;
 }
 
 __device__ __forceinline__ void put(float* c, float v) { *c = v; }
 __device__ __forceinline__ void put(__nv_bfloat16* c, float v) { *c = __float2bfloat16_rn(v); }
 
-// One element of C from its finished sum.
+// One element of C from its finished sum (already over the temperature).
 template <typename O>
 __device__ __forceinline__ void finish(const ProductArgs& p, int m, int n, float v) {
-  if (p.tau) v = __fdiv_rn(v, __ldg(p.tau + m));
   O* c = static_cast<O*>(p.C) + (int64_t)m * p.ldc + n;
   if (p.accumulate) v += (float)*c;
   put(c, v);
 }
 
-template <int NT, typename O>
-__global__ void __launch_bounds__(kThreads, 1)
-    product_kernel(const __grid_constant__ CUtensorMap map_b,
-                   const __grid_constant__ CUtensorMap map_a, const ProductArgs p) {
-  using S = Shape<NT>;
-  constexpr int kBufs = S::kBufs, kStages = S::kStages;
-  constexpr int kHalf = NT / 2;
-  constexpr int kChunk = kHalf < 32 ? kHalf : 32;
-  extern __shared__ uint8_t smem_raw[];
-  const uint32_t raw_s = smem_u32(smem_raw);
-  uint8_t* smem = smem_raw + ((1024u - (raw_s & 1023u)) & 1023u);
+// 1 / tau_m, by which row m's sums are multiplied.
+__device__ __forceinline__ float over_tau(const ProductArgs& p, int m) {
+  return p.tau ? __frcp_rn(__ldg(p.tau + m)) : 1.f;
+}
 
-  uint8_t* sB = smem;
-  uint8_t* sA = sB + kStages * S::kBytesB;
-  float* sS = reinterpret_cast<float*>(sA + kStages * S::kBytesA);
-  uint64_t* full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(sS) +
-                                               kScaleSlots * S::kSlot);
+// The wide form's sums take 208 registers a thread and its other warps 64:
+// 128 x 64 + 256 x 208 = 61,440 of the launch's 384 x 168 = 64,512. Each is
+// called at one place by whole warpgroups, inside the branch that needs it (code
+// that follows both branches is bound to the smaller number).
+template <bool kWide>
+__device__ __forceinline__ void give_registers() {
+  if constexpr (kWide) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+}
+template <bool kWide>
+__device__ __forceinline__ void take_registers() {
+  if constexpr (kWide) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+}
+
+template <int NT, bool kWide, bool kUniform, typename O>
+__global__ void __launch_bounds__(kThreads, 1)
+    product_kernel(const __grid_constant__ CUtensorMap map_l,
+                   const __grid_constant__ CUtensorMap map_c,
+                   const __grid_constant__ CUtensorMap map_out, const ProductArgs p) {
+  using S = Shape<NT, kWide, kUniform>;
+  constexpr int kBufs = S::kBufs, kStages = S::kStages, kSlots = S::kSlots;
+  constexpr int kHalf = NT / 2;
+  // columns in flight from tensor memory, twice (beside the sums, and the
+  // columns' scales where they differ)
+  constexpr int kMostChunk = kUniform ? 32 : 16;
+  constexpr int kChunk = kHalf < kMostChunk ? kHalf : kMostChunk;
+  extern __shared__ __align__(1024) uint8_t smem[];
+
+  uint8_t* sL = smem;
+  uint8_t* sC = sL + kStages * S::kLaneBytes;
+  uint8_t* staging = sC + kStages * S::kColBytes;
+  float* sS = reinterpret_cast<float*>(staging + S::kStagingBytes);
+  uint64_t* full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(sS) + kSlots * S::kSlot);
   uint64_t* empty = full + kStages;
   uint64_t* sfull = empty + kStages;
-  uint64_t* sempty = sfull + kScaleSlots;
-  uint64_t* tfull = sempty + kScaleSlots;
+  uint64_t* sempty = sfull + kSlots;
+  uint64_t* tfull = sempty + kSlots;
   uint64_t* tempty = tfull + kBufs;
   uint64_t* drain = tempty + kBufs;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
@@ -188,7 +336,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const int tiles = p.tiles_m * p.tiles_n;
+  const int tiles = p.tiles_l * p.tiles_c;
   // this CTA's stretch of k, and its first tile and tile stride
   const int part = blockIdx.x % p.split;
   const int kb0 = (int)((int64_t)p.kb * part / p.split);
@@ -201,7 +349,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&full[s]), 1);
       mbar_init(smem_u32(&empty[s]), 1);
     }
-    for (int s = 0; s < kScaleSlots; ++s) {
+    for (int s = 0; s < kSlots; ++s) {
       mbar_init(smem_u32(&sfull[s]), 32);
       mbar_init(smem_u32(&sempty[s]), kSumWarps);
     }
@@ -210,13 +358,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&tempty[b]), kSumWarps);
     }
     mbar_init(smem_u32(drain), 1);
-    *abort_flag = 0;
+    // the ring's swizzle needs 1,024-byte stages; without them nothing runs
+    *abort_flag = (smem_u32(smem) & 1023u) != 0 ? 1 : 0;
+    if (*abort_flag && p.err) atomicCAS(p.err, 0, (int)STS_ERR_OVERFLOW);
     fence_barrier_init();
     fence_proxy_async_smem();
   }
   if (warp == 0 && lane == 0) {
-    tma_prefetch_desc(&map_b);
-    tma_prefetch_desc(&map_a);
+    tma_prefetch_desc(&map_l);
+    tma_prefetch_desc(&map_c);
+    if (kWide && p.tma_out) tma_prefetch_desc(&map_out);
   }
   if (warp == 1) {
     tmem_alloc(smem_u32(tmem_holder), S::kTmemCols);
@@ -226,207 +377,346 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
+  const bool start_ok = *abort_flag == 0;
 
-  // this thread's sums (warps 2..9): row n of the tile, kHalf columns m
-  float acc[kHalf];
   const int quarter = warp & 3;
-  const int half = warp >= 6 ? 1 : 0;
-  int last_tm = 0, last_tn = 0;
+  const int half = warp >= 8 ? 1 : 0;
+  int last_l = 0, last_c = 0;
   bool have = false;
 
+  // Warps 0 and 1 have 512 clocks (wide) for a block: their loops go through one
+  // turn of the rings at a time, so that barriers, addresses and phases are
+  // constants, and count blocks through the tiles' ends.
+  const int mine_tiles = tile0 < tiles ? (tiles - tile0 + step - 1) / step : 0;
+  const int blocks = mine_tiles * (kb1 - kb0);
+  if (warp < 4) {
+  give_registers<kWide>();
   if (warp == 0) {
-    // ------------------------------------------------------------ producer
-    uint32_t stage = 0, phase = 0, slot = 0, sphase = 0;
-    long long issued = 0;
-    bool ok = true;
-    for (int t = tile0; ok && t < tiles; t += step) {
-      int tm, tn;
-      tile_coords(t, p.tiles_m, p.tiles_n, tm, tn);
-      for (int kb = kb0; kb < kb1; ++kb) {
-        if (!mbar_wait(smem_u32(&empty[stage]), phase ^ 1u, abort_flag, p.err)) {
+    // ------------------------------------------------------------ operands
+    const uint32_t mine = elected();
+    const uint32_t bytes = (uint32_t)(p.height + NT) * kBlock;
+    int t = tile0, kb = kb0, tl, tc;
+    tile_coords<kWide>(p, t, tl, tc);
+    bool ok = start_ok;
+    int done = 0;
+    for (uint32_t phase = 1; ok && done < blocks; phase ^= 1u) {
+#pragma unroll
+      for (int s = 0; s < kStages; ++s) {
+        if (done >= blocks) break;
+        if (!mbar_wait_soon(smem_u32(&empty[s]), phase, abort_flag, p.err)) {
           ok = false;
           break;
         }
-        if (lane == 0) {
-          const uint32_t fb = smem_u32(&full[stage]);
-          mbar_arrive_expect_tx(fb, S::kStage);
-          tma_load_2d(smem_u32(sB + stage * S::kBytesB), &map_b, fb, kb * kBlock, tn * kRowsB);
-          tma_load_2d(smem_u32(sA + stage * S::kBytesA), &map_a, fb, kb * kBlock, tm * NT);
+        load_stage(mine, smem_u32(&full[s]), bytes, smem_u32(sL + s * S::kLaneBytes), &map_l,
+                   tl * p.height, smem_u32(sC + s * S::kColBytes), &map_c, tc * NT, kb * kBlock);
+        ++done;
+        if (++kb == kb1) {
+          kb = kb0;
+          t += step;
+          tile_coords<kWide>(p, t, tl, tc);
         }
-        __syncwarp();
-        ++issued;
-        if (++stage == kStages) {
-          stage = 0;
-          phase ^= 1u;
+      }
+    }
+    // Our own loads must have landed before the CTA may exit.
+    for (int s = 0; s < kStages; ++s)
+      if (done > s) mbar_wait_drain(smem_u32(&full[s]), (uint32_t)((done - 1 - s) / kStages) & 1u);
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ MMA issuer
+    const uint32_t mine = elected();
+    const uint64_t rows0 = desc_kmajor_sw128(smem_u32(sL)), cols0 = desc_kmajor_sw128(smem_u32(sC));
+    constexpr int kTurn = S::kTurn;
+    bool ok = start_ok;
+    int done = 0;
+    // phases at the start of a turn; within it they change as the rings wrap
+    for (uint32_t fphase = 0, tphase = 1; ok && done < blocks;
+         fphase ^= (kTurn / kStages) & 1, tphase ^= (kTurn / kBufs) & 1) {
+#pragma unroll
+      for (int i = 0; i < kTurn; ++i) {
+        const int s = i % kStages, b = i % kBufs;
+        if (done >= blocks) break;
+        if (!mbar_wait_soon(smem_u32(&tempty[b]), tphase ^ ((i / kBufs) & 1), abort_flag, p.err) ||
+            !mbar_wait_soon(smem_u32(&full[s]), fphase ^ ((i / kStages) & 1), abort_flag, p.err)) {
+          ok = false;
+          break;
         }
-        if (!mbar_wait(smem_u32(&sempty[slot]), sphase ^ 1u, abort_flag, p.err)) {
+        tc_fence_after();
+        umma_block(mine, tmem_base + b * NT, rows0 + s * (S::kLaneBytes >> 4),
+                   cols0 + s * (S::kColBytes >> 4), p.idesc);
+        commit(mine, smem_u32(&tfull[b]));
+        commit(mine, smem_u32(&empty[s]));
+        ++done;
+      }
+    }
+    // Every MMA this warp issued must be complete before TMEM is freed.
+    commit(mine, smem_u32(drain));
+    mbar_wait_drain(smem_u32(drain), 0);
+  } else if (warp == 2) {
+    // ------------------------------------------------------------ scales
+    uint32_t slot = 0, sphase = 0;
+    bool ok = start_ok;
+    for (int t = tile0; ok && t < tiles; t += step) {
+      int tl, tc;
+      tile_coords<kWide>(p, t, tl, tc);
+      // this thread's rows of both operands: where their scales start, or null
+      const float* ls[kLanes / 32];
+      const float* cs[S::kColScales < 32 ? 1 : S::kColScales / 32];
+#pragma unroll
+      for (int i = 0; i < kLanes / 32; ++i) {
+        const int j = i * 32 + lane, row = tl * p.height + j;
+        ls[i] = j < p.height && row < p.lane_n
+                    ? p.lane_scale + (int64_t)(row >> p.lane_shift) * p.lane_sr
+                    : nullptr;
+      }
+      if constexpr (kUniform) {
+        const int row = tc * NT + lane * kBlock;
+        cs[0] = lane < NT / kBlock && row < p.col_n
+                    ? p.col_scale + (int64_t)(row / kBlock) * p.col_sr
+                    : nullptr;
+      } else {
+#pragma unroll
+        for (int i = 0; i < (NT + 31) / 32; ++i) {
+          const int j = i * 32 + lane, row = tc * NT + j;
+          cs[i] = j < NT && row < p.col_n ? p.col_scale + (int64_t)row * p.col_sr : nullptr;
+        }
+      }
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!mbar_wait_soon(smem_u32(&sempty[slot]), sphase ^ 1u, abort_flag, p.err)) {
           ok = false;
           break;
         }
         const uint32_t dst = smem_u32(sS) + slot * S::kSlot;
 #pragma unroll
-        for (int i = 0; i < (NT + 31) / 32; ++i) {
-          const int j = i * 32 + lane, m = tm * NT + j;
-          if (j < NT) {
-            const bool live = m < p.M;
-            copy4(dst + j * 4, p.a_scale + (live ? m * p.a_sr + kb * p.a_sk : 0), live);
-          }
-        }
-        if (p.b_shared) {
-          if (lane == 0) copy4(dst + NT * 4, p.b_scale + tn * p.b_sr + kb * p.b_sk, true);
+        for (int i = 0; i < kLanes / 32; ++i)
+          copy4(dst + (i * 32 + lane) * 4, ls[i] ? ls[i] + kb * p.lane_sk : p.lane_scale,
+                ls[i] != nullptr);
+        if constexpr (kUniform) {
+          if (lane < NT / kBlock)
+            copy4(dst + (kLanes + lane) * 4, cs[0] ? cs[0] + kb * p.col_sk : p.col_scale,
+                  cs[0] != nullptr);
         } else {
 #pragma unroll
-          for (int i = 0; i < kRowsB / 32; ++i) {
-            const int j = i * 32 + lane, n = tn * kRowsB + j;
-            const bool live = n < p.N;
-            copy4(dst + (NT + j) * 4, p.b_scale + (live ? n * p.b_sr + kb * p.b_sk : 0), live);
-          }
+          for (int i = 0; i < (NT + 31) / 32; ++i)
+            if (i * 32 + lane < NT)
+              copy4(dst + (kLanes + i * 32 + lane) * 4, cs[i] ? cs[i] + kb * p.col_sk : p.col_scale,
+                    cs[i] != nullptr);
         }
         copies_arrive(smem_u32(&sfull[slot]));
-        if (++slot == kScaleSlots) {
+        if (++slot == kSlots) {
           slot = 0;
           sphase ^= 1u;
         }
       }
     }
-    // Our own loads must have landed before the CTA may exit.
-    asm volatile("cp.async.wait_all;" ::: "memory");
-    if (lane == 0) {
-      for (int s = 0; s < kStages; ++s) {
-        if (issued > s) {
-          const long long last = ((issued - 1 - s) / kStages) * kStages + s;
-          mbar_wait_drain(smem_u32(&full[s]), (uint32_t)((last / kStages) & 1));
-        }
-      }
-    }
-    __syncwarp();
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer
-    uint32_t stage = 0, phase = 0, buf = 0, bphase = 0;
-    bool ok = true;
-    for (int t = tile0; ok && t < tiles; t += step) {
-      for (int kb = kb0; kb < kb1; ++kb) {
-        if (!mbar_wait(smem_u32(&tempty[buf]), bphase ^ 1u, abort_flag, p.err) ||
-            !mbar_wait(smem_u32(&full[stage]), phase, abort_flag, p.err)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        if (lane == 0) {
-          const uint32_t rows = smem_u32(sB + stage * S::kBytesB);
-          const uint32_t cols = smem_u32(sA + stage * S::kBytesA);
-#pragma unroll
-          for (int kk = 0; kk < kBlock / 32; ++kk)
-            umma_f8(tmem_base + buf * NT, desc_kmajor_sw128(rows + kk * 32),
-                    desc_kmajor_sw128(cols + kk * 32), p.idesc, kk != 0 ? 1u : 0u);
-          umma_commit(smem_u32(&empty[stage]));
-          umma_commit(smem_u32(&tfull[buf]));
-        }
-        __syncwarp();
-        if (++stage == kStages) {
-          stage = 0;
-          phase ^= 1u;
-        }
-        if (++buf == kBufs) {
-          buf = 0;
-          bphase ^= 1u;
-        }
-      }
-    }
-    // Every MMA this thread issued must be complete before TMEM is freed.
-    if (lane == 0) {
-      umma_commit(smem_u32(drain));
-      mbar_wait_drain(smem_u32(drain), 0);
-    }
-    __syncwarp();
+    asm volatile("cp.async.wait_all;" ::: "memory");  // before the CTA may exit
+  }
   } else {
     // ------------------------------------------------------------ scale and sum
+    take_registers<kWide>();
+    uint64_t acc[kHalf / 2];  // this thread's sums: its lane's row, kHalf columns, in pairs
     uint32_t slot = 0, sphase = 0, buf = 0, bphase = 0;
-    bool ok = true;
+    uint32_t sel = 0;
+    bool ok = start_ok;
     for (int t = tile0; ok && t < tiles; t += step) {
-      int tm, tn;
-      tile_coords(t, p.tiles_m, p.tiles_n, tm, tn);
+      int tl, tc;
+      tile_coords<kWide>(p, t, tl, tc);
 #pragma unroll
-      for (int j = 0; j < kHalf; ++j) acc[j] = 0.f;
-      for (int kb = kb0; kb < kb1; ++kb) {
-        if (!mbar_wait(smem_u32(&sfull[slot]), sphase, abort_flag, p.err) ||
-            !mbar_wait(smem_u32(&tfull[buf]), bphase, abort_flag, p.err)) {
-          ok = false;
-          break;
-        }
+      for (int j = 0; j < kHalf / 2; ++j) acc[j] = 0;
+      // The loads of a block's first columns are issued ahead, while the last
+      // columns of the block before are summed, where it is ready by then.
+      uint32_t r[2][kChunk];
+      float s = 0.f;
+      const float* sc = nullptr;
+      const uint32_t lane_addr = tmem_base + ((uint32_t)(quarter * 32) << 16) + half * kHalf;
+      auto begin = [&]() {  // the block at (slot, buf) is ready
         tc_fence_after();
-        const float* sa = sS + slot * (S::kSlot / 4) + half * kHalf;
-        const float* sb = sS + slot * (S::kSlot / 4) + NT;
-        const float b = sb[p.b_shared ? 0 : quarter * 32 + lane];
-        const uint32_t taddr = tmem_base + ((uint32_t)(quarter * 32) << 16) + buf * NT + half * kHalf;
+        const float* sl = sS + slot * (S::kSlot / 4);
+        sc = sl + kLanes + (kUniform ? half : half * kHalf);
+        s = sl[quarter * 32 + lane];
+        if constexpr (kUniform) s *= sc[0];
+        tmem_ld<kChunk>(lane_addr + buf * NT, r[0]);
+      };
+      auto wait = [&]() {
+        return mbar_wait_soon(smem_u32(&sfull[slot]), sphase, abort_flag, p.err) &&
+               mbar_wait_soon(smem_u32(&tfull[buf]), bphase, abort_flag, p.err);
+      };
+      ok = kb0 < kb1 && wait();
+      if (!ok) break;
+      begin();
+      for (int kb = kb0; kb < kb1; ++kb) {
+        const uint64_t s2 = pair(s, s);
+        constexpr int kSteps = kHalf / kChunk;
+        static_assert(kSteps == 1 || kSteps % 2 == 0, "the next block starts in r[0]");
+        bool ahead = true;
 #pragma unroll
-        for (int c0 = 0; c0 < kHalf; c0 += kChunk) {
-          uint32_t r[kChunk];
-          tmem_ld<kChunk>(taddr + c0, r);
-          tmem_ld_wait();
+        for (int c = 0; c < kSteps; ++c) {
+          uint32_t(&v)[kChunk] = r[c & 1];
+          float4 b[kUniform ? 1 : kChunk / 4];
+          if constexpr (!kUniform) {  // on their way while tensor memory answers
 #pragma unroll
-          for (int j = 0; j < kChunk; j += 4) {
-            const float4 a = *reinterpret_cast<const float4*>(sa + c0 + j);
-            acc[c0 + j] = fmaf(__uint_as_float(r[j]), a.x * b, acc[c0 + j]);
-            acc[c0 + j + 1] = fmaf(__uint_as_float(r[j + 1]), a.y * b, acc[c0 + j + 1]);
-            acc[c0 + j + 2] = fmaf(__uint_as_float(r[j + 2]), a.z * b, acc[c0 + j + 2]);
-            acc[c0 + j + 3] = fmaf(__uint_as_float(r[j + 3]), a.w * b, acc[c0 + j + 3]);
+            for (int j = 0; j < kChunk / 4; ++j)
+              b[j] = *reinterpret_cast<const float4*>(sc + c * kChunk + 4 * j);
+          }
+          tmem_wait<kChunk>(v);
+          if (c + 1 < kSteps) {
+            tmem_ld<kChunk>(lane_addr + buf * NT + (c + 1) * kChunk, r[(c + 1) & 1]);
+          } else {  // the block is in registers: its accumulator and scales are free
+            if constexpr (kSteps == 1) {
+#pragma unroll
+              for (int j = 0; j < kChunk; ++j) r[1][j] = r[0][j];
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(smem_u32(&tempty[buf]));
+              mbar_arrive(smem_u32(&sempty[slot]));
+            }
+            if (++slot == kSlots) {
+              slot = 0;
+              sphase ^= 1u;
+            }
+            if (++buf == kBufs) {
+              buf = 0;
+              bphase ^= 1u;
+            }
+            if (kb + 1 < kb1) {
+              ahead = __all_sync(0xFFFFFFFFu, mbar_test(smem_u32(&sfull[slot]), sphase) &&
+                                                  mbar_test(smem_u32(&tfull[buf]), bphase));
+              if (ahead) begin();
+            }
+          }
+          uint32_t(&w)[kChunk] = r[kSteps == 1 ? 1 : c & 1];
+#pragma unroll
+          for (int j = 0; j < kChunk / 4; ++j) {
+            uint64_t& a0 = acc[(c * kChunk + 4 * j) / 2];
+            uint64_t& a1 = acc[(c * kChunk + 4 * j) / 2 + 1];
+            if constexpr (kUniform) {
+              a0 = fma2(pair(w[4 * j], w[4 * j + 1]), s2, a0);
+              a1 = fma2(pair(w[4 * j + 2], w[4 * j + 3]), s2, a1);
+            } else {
+              a0 = fma2(pair(w[4 * j], w[4 * j + 1]), mul2(pair(b[j].x, b[j].y), s2), a0);
+              a1 = fma2(pair(w[4 * j + 2], w[4 * j + 3]), mul2(pair(b[j].z, b[j].w), s2), a1);
+            }
           }
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(smem_u32(&tempty[buf]));
-          mbar_arrive(smem_u32(&sempty[slot]));
-        }
-        if (++slot == kScaleSlots) {
-          slot = 0;
-          sphase ^= 1u;
-        }
-        if (++buf == kBufs) {
-          buf = 0;
-          bphase ^= 1u;
+        if (!ahead) {
+          ok = wait();
+          if (!ok) break;
+          begin();
         }
       }
       if (!ok) break;
-      if (p.split == 1) {
-        const int n = tn * kRowsB + quarter * 32 + lane;
-        const int m0 = tm * NT + half * kHalf;
-        if (n < p.N) {
+      if (p.split > 1) {
+        last_l = tl;
+        last_c = tc;
+        have = true;
+      } else if constexpr (!kWide) {
+        const int row = quarter * 32 + lane;
+        const int n = tl * p.height + row;
+        const int m0 = tc * NT + half * kHalf;
+        const bool mine = row < p.height && n < p.N;
 #pragma unroll
-          for (int j = 0; j < kHalf; ++j)
-            if (m0 + j < p.M) finish<O>(p, m0 + j, n, acc[j]);
+        for (int j = 0; j < kHalf / 2; ++j) {
+          const float2 v = unpair(acc[j]);
+          if (m0 + 2 * j < p.M && mine)
+            finish<O>(p, m0 + 2 * j, n, v.x * over_tau(p, m0 + 2 * j));
+          if (m0 + 2 * j + 1 < p.M && mine)
+            finish<O>(p, m0 + 2 * j + 1, n, v.y * over_tau(p, m0 + 2 * j + 1));
         }
       } else {
-        last_tm = tm;
-        last_tn = tn;
-        have = true;
+        // 32 rows x 64 bytes at a time: a thread's row in 16-byte pieces, piece
+        // i of row r at i ^ (r / 2) % 4 (64-byte swizzle, no bank conflicts)
+        constexpr int kCols = 64 / (int)sizeof(O);
+        const int m0 = tl * kLanes + quarter * 32, m = m0 + lane;
+        const float inv = m < p.M ? over_tau(p, m) : 0.f;
+        uint8_t* mine = staging + (warp - 4) * 2 * kStaging;
+#pragma unroll
+        for (int c = 0; c < kHalf / kCols; ++c) {
+          const int n0 = tc * NT + half * kHalf + c * kCols;
+          if (n0 < p.N && m0 < p.M) {  // the same in every thread of the warp
+            const uint32_t buf_s = smem_u32(mine + sel * kStaging);
+            if (lane == 0) bulk_wait_read<1>();
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint32_t w[4];
+              if constexpr (sizeof(O) == 4) {
+                const float2 x = unpair(acc[c * 8 + 2 * i]), y = unpair(acc[c * 8 + 2 * i + 1]);
+                w[0] = __float_as_uint(x.x * inv);
+                w[1] = __float_as_uint(x.y * inv);
+                w[2] = __float_as_uint(y.x * inv);
+                w[3] = __float_as_uint(y.y * inv);
+              } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  const float2 x = unpair(acc[c * 16 + 4 * i + k]);
+                  w[k] = pack_bf16x2(x.x * inv, x.y * inv);
+                }
+              }
+              st_shared_v4(buf_s + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4), w[0], w[1], w[2], w[3]);
+            }
+            if (p.tma_out) {
+              fence_proxy_async_smem();
+              __syncwarp();
+              if (lane == 0) {
+                if (p.accumulate)
+                  tma_reduce_add_2d(&map_out, buf_s, n0, m0);
+                else
+                  tma_store_2d(&map_out, buf_s, n0, m0);
+                bulk_commit();
+              }
+            } else {  // rows of C that TMA cannot address: 64 bytes of a row per 16 or 32 lanes
+              __syncwarp();
+              constexpr int kRows = 32 / kCols;  // rows per step
+              const int col = lane % kCols;
+              for (int r = lane / kCols; r < 32; r += kRows) {
+                const O v = *reinterpret_cast<const O*>(
+                    mine + sel * kStaging + r * 64 +
+                    (((col * (int)sizeof(O) / 16) ^ ((r >> 1) & 3)) << 4) + (col * (int)sizeof(O)) % 16);
+                if (m0 + r < p.M && n0 + col < p.N) finish<O>(p, m0 + r, n0 + col, (float)v);
+              }
+              __syncwarp();
+            }
+            sel ^= 1u;
+          }
+        }
+      }
+    }
+    if (kWide && lane == 0) bulk_wait_all();
+    __syncwarp();
+    if (have) {
+      // One tile per cluster. Every stage has been read by now (the sums wait
+      // for the last MMA), so the ring holds the sums, kPitch floats a lane.
+      float* mine = reinterpret_cast<float*>(smem) + (quarter * 32 + lane) * S::kPitch + half * kHalf;
+#pragma unroll
+      for (int j = 0; j < kHalf / 2; ++j) {
+        const float2 v = unpair(acc[j]);
+        mine[2 * j] = v.x;
+        mine[2 * j + 1] = v.y;
       }
     }
   }
 
   if (p.split > 1) {
-    // One tile per cluster. Every stage has been read by now (the sums wait for
-    // the last MMA), so the ring holds the sums: [column][row of the tile].
-    __syncthreads();
-    float* sums = reinterpret_cast<float*>(smem);
-    if (warp >= 2 && have) {
-#pragma unroll
-      for (int j = 0; j < kHalf; ++j)
-        sums[(half * kHalf + j) * kRowsB + quarter * 32 + lane] = acc[j];
-    }
+    const float* sums = reinterpret_cast<const float*>(smem);
+    constexpr int kPitch = S::kPitch;
     cg::cluster_group cluster = cg::this_cluster();
     cluster.sync();
-    if (warp >= 2 && have) {
-      const int c1 = NT / p.split * (part + 1);
-      const int n = last_tn * kRowsB + quarter * 32 + lane;
-      for (int j = NT / p.split * part + half; j < c1; j += 2) {
-        const int m = last_tm * NT + j;
+    if (warp >= 4 && have) {
+      // the CTAs divide the lines that C's rows want written: one m, consecutive
+      // n (wide: a lane's sums; narrow: a column's)
+      constexpr int kLines = kWide ? kLanes : NT, kLong = kWide ? NT : kLanes;
+      for (int j = part + p.split * (warp - 4); j < kLines; j += p.split * kSumWarps) {
+        const int m = (kWide ? last_l * kLanes : last_c * NT) + j;
         if (m >= p.M) break;
-        float v = 0.f;
-        for (int q = 0; q < p.split; ++q)
-          v += cluster.map_shared_rank(sums, q)[j * kRowsB + quarter * 32 + lane];
-        if (n < p.N) finish<O>(p, m, n, v);
+        const float inv = over_tau(p, m);
+        const int n0 = kWide ? last_c * NT : last_l * p.height;
+        const int end = min(kWide ? kLong : p.height, p.N - n0);
+        for (int i = lane; i < end; i += 32) {
+          const int at = kWide ? j * kPitch + i : i * kPitch + j;
+          float v = 0.f;
+          for (int q = 0; q < p.split; ++q) v += cluster.map_shared_rank(sums, q)[at];
+          finish<O>(p, m, n0 + i, v * inv);
+        }
       }
     }
     cluster.sync();
@@ -438,17 +728,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int NT, typename O>
-cudaError_t launch(const CUtensorMap& mb, const CUtensorMap& ma, const ProductArgs& p, int grid,
-                   cudaStream_t st) {
-  auto kern = product_kernel<NT, O>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)Shape<NT>::kSmem);
+struct Maps {
+  CUtensorMap lanes, cols, out;
+};
+
+template <int NT, bool kWide, bool kUniform, typename O>
+cudaError_t launch(const Maps& maps, const ProductArgs& p, int grid, cudaStream_t st) {
+  using S = Shape<NT, kWide, kUniform>;
+  auto kern = product_kernel<NT, kWide, kUniform, O>;
+  cudaError_t e =
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = Shape<NT>::kSmem;
+  cfg.dynamicSmemBytes = S::kSmem;
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
@@ -457,25 +751,33 @@ cudaError_t launch(const CUtensorMap& mb, const CUtensorMap& ma, const ProductAr
   at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = p.split > 1 ? 1 : 0;
-  e = cudaLaunchKernelEx(&cfg, kern, mb, ma, p);
+  e = cudaLaunchKernelEx(&cfg, kern, maps.lanes, maps.cols, maps.out, p);
   const cudaError_t last = cudaGetLastError();
   return e != cudaSuccess ? e : last;
 }
 
-template <int NT>
-cudaError_t launch_out(bool bf16, const CUtensorMap& mb, const CUtensorMap& ma,
-                       const ProductArgs& p, int grid, cudaStream_t st) {
-  return bf16 ? launch<NT, __nv_bfloat16>(mb, ma, p, grid, st)
-              : launch<NT, float>(mb, ma, p, grid, st);
+template <typename O>
+cudaError_t launch_out(int NT, bool uniform, const Maps& maps, const ProductArgs& p, int grid,
+                       cudaStream_t st) {
+  switch (NT) {
+    case 16: return launch<16, false, false, O>(maps, p, grid, st);
+    case 32: return launch<32, false, false, O>(maps, p, grid, st);
+    case 64: return launch<64, false, false, O>(maps, p, grid, st);
+    case 128: return launch<128, false, false, O>(maps, p, grid, st);
+    default:
+      return uniform ? launch<256, true, true, O>(maps, p, grid, st)
+                     : launch<256, true, false, O>(maps, p, grid, st);
+  }
 }
 
 constexpr int64_t kMost = (int64_t(1) << 31) - 1024;
+constexpr int kMinHeight = 16;  // rows of B in the narrow form's smallest tile
 
 sts_status check_operand(const sts_block_operand* o, int64_t K, bool rows_only) {
   if (!o) return STS_ERR_NULL;
   if (o->dtype != STS_DTYPE_E4M3 && o->dtype != STS_DTYPE_E5M2) return STS_ERR_DTYPE;
   if (o->rows < 0 || o->rows > kMost) return STS_ERR_SHAPE;
-  if (o->block_rows != 1 && (rows_only || o->block_rows != kRowsB)) return STS_ERR_SHAPE;
+  if (o->block_rows != 1 && (rows_only || o->block_rows != kBlock)) return STS_ERR_SHAPE;
   if (o->scale_stride_r < 0 || o->scale_stride_k < 0) return STS_ERR_SHAPE;
   if (o->rows == 0) return STS_OK;
   if (!o->q || !o->scale) return STS_ERR_NULL;
@@ -516,29 +818,41 @@ extern "C" sts_status sts_block_scaled_product(const sts_block_operand* A,
   if (s != STS_OK) return s;
 
   const int64_t M = A->rows, N = B->rows;
-  const int NT = M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : M <= 128 ? 128 : 256;
+  const bool wide = M > kLanes;
+  const int NT = wide ? 256 : M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
+  const sts_block_operand* L = wide ? A : B;  // the lanes' operand
+  const sts_block_operand* R = wide ? B : A;  // the columns'
+  const bool uniform = wide && B->block_rows == kBlock;
   ProductArgs p{};
   p.M = (int)M;
   p.N = (int)N;
-  p.K = (int)K;
   p.kb = (int)((K + kBlock - 1) / kBlock);
-  const int64_t tiles_m = (M + NT - 1) / NT, tiles_n = (N + kRowsB - 1) / kRowsB;
-  if (tiles_m * tiles_n > kMost) return STS_ERR_SHAPE;
-  p.tiles_m = (int)tiles_m;
-  p.tiles_n = (int)tiles_n;
-  p.a_scale = A->scale;
-  p.a_sr = A->scale_stride_r;
-  p.a_sk = A->scale_stride_k;
-  p.b_scale = B->scale;
-  p.b_sr = B->scale_stride_r;
-  p.b_sk = B->scale_stride_k;
-  p.b_shared = B->block_rows == kRowsB ? 1 : 0;
-  p.idesc = idesc_f8(B->dtype == STS_DTYPE_E5M2, A->dtype == STS_DTYPE_E5M2, kRowsB, NT);
+  p.lane_n = (int)L->rows;
+  p.col_n = (int)R->rows;
+  p.height = kLanes;
+  if (!wide) {
+    // as many rounds of tiles as 128 rows each would take, and equal tiles
+    const int64_t rounds = (N + (int64_t)kLanes * sms - 1) / ((int64_t)kLanes * sms);
+    p.height = (int)((N + rounds * sms - 1) / (rounds * sms));
+    if (p.height < kMinHeight) p.height = kMinHeight;
+  }
+  const int64_t tiles_l = (L->rows + p.height - 1) / p.height, tiles_c = (R->rows + NT - 1) / NT;
+  if (tiles_l * tiles_c > kMost) return STS_ERR_SHAPE;
+  p.tiles_l = (int)tiles_l;
+  p.tiles_c = (int)tiles_c;
+  p.lane_scale = L->scale;
+  p.lane_sr = L->scale_stride_r;
+  p.lane_sk = L->scale_stride_k;
+  p.lane_shift = L->block_rows == kBlock ? 7 : 0;
+  p.col_scale = R->scale;
+  p.col_sr = R->scale_stride_r;
+  p.col_sk = R->scale_stride_k;
+  p.idesc = idesc_f8(L->dtype == STS_DTYPE_E5M2, R->dtype == STS_DTYPE_E5M2, kLanes, NT);
   p.tau = temperature;
   p.C = C;
   p.ldc = ldc;
   p.accumulate = accumulate ? 1 : 0;
-  const int64_t tiles = tiles_m * tiles_n;
+  const int64_t tiles = tiles_l * tiles_c;
   p.split = 1;
   while (p.split < kMaxSplit && tiles * p.split * 2 <= sms && p.kb >= p.split * 2 * 4) p.split *= 2;
   const int grid = (int)(p.split > 1 ? tiles * p.split : (tiles < sms ? tiles : sms));
@@ -551,19 +865,28 @@ extern "C" sts_status sts_block_scaled_product(const sts_block_operand* A,
       return STS_ERR_CUDA;
     p.err = &hdr->err;
   }
-  CUtensorMap ma, mb;
-  if (!tensor_map_2d(&mb, B->q, CU_TENSOR_MAP_DATA_TYPE_UINT8, (uint64_t)K, (uint64_t)N,
-                     (uint64_t)B->ld, kBlock, kRowsB) ||
-      !tensor_map_2d(&ma, A->q, CU_TENSOR_MAP_DATA_TYPE_UINT8, (uint64_t)K, (uint64_t)M,
-                     (uint64_t)A->ld, kBlock, (uint32_t)NT))
-    return STS_ERR_CUDA;
-  const LaunchMark mark = launch_begin(STS_KERNEL_BLOCK_PRODUCT, st);
   const bool bf = c_dtype == STS_DTYPE_BF16;
-  const cudaError_t e = NT == 16    ? launch_out<16>(bf, mb, ma, p, grid, st)
-                        : NT == 32  ? launch_out<32>(bf, mb, ma, p, grid, st)
-                        : NT == 64  ? launch_out<64>(bf, mb, ma, p, grid, st)
-                        : NT == 128 ? launch_out<128>(bf, mb, ma, p, grid, st)
-                                    : launch_out<256>(bf, mb, ma, p, grid, st);
+  const int64_t cs = bf ? 2 : 4;
+  Maps maps;
+  std::memset(&maps, 0, sizeof(maps));
+  if (!tensor_map_2d(&maps.lanes, L->q, CU_TENSOR_MAP_DATA_TYPE_UINT8, (uint64_t)K,
+                     (uint64_t)L->rows, (uint64_t)L->ld, kBlock, (uint32_t)p.height,
+                     CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !tensor_map_2d(&maps.cols, R->q, CU_TENSOR_MAP_DATA_TYPE_UINT8, (uint64_t)K,
+                     (uint64_t)R->rows, (uint64_t)R->ld, kBlock, (uint32_t)NT,
+                     CU_TENSOR_MAP_SWIZZLE_128B))
+    return STS_ERR_CUDA;
+  if (wide && (reinterpret_cast<uintptr_t>(C) & 15u) == 0 && ldc * cs % 16 == 0 &&
+      ldc < (int64_t(1) << 37)) {
+    if (!tensor_map_2d(&maps.out, C, bf ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
+                       (uint64_t)N, (uint64_t)M, (uint64_t)(ldc * cs), (uint32_t)(64 / cs), 32,
+                       CU_TENSOR_MAP_SWIZZLE_64B))
+      return STS_ERR_CUDA;
+    p.tma_out = 1;
+  }
+  const LaunchMark mark = launch_begin(STS_KERNEL_BLOCK_PRODUCT, st);
+  const cudaError_t e = bf ? launch_out<__nv_bfloat16>(NT, uniform, maps, p, grid, st)
+                           : launch_out<float>(NT, uniform, maps, p, grid, st);
   launch_end(mark, st);
   return e == cudaSuccess ? STS_OK : STS_ERR_CUDA;
 }

@@ -4,9 +4,12 @@
 // For a block with largest finite magnitude a, and top the largest code of the
 // 8-bit type (448 for e4m3, 57344 for e5m2):
 //   scale = a / top, or 1 when that quotient is 0   (IEEE fp32 division)
-//   code  = x / scale, IEEE fp32 division, limited to +-top, rounded to nearest
-//           even in the 8-bit type; NaN for an x that is not finite
-// so that code * scale is x within half a step of the 8-bit type (2^-4
+//   code  = x (1 / scale), the reciprocal and the product rounded to fp32 (x /
+//           scale where scale is below 2^-126, whose reciprocal may not exist),
+//           limited to +-top, rounded to nearest even in the 8-bit type; NaN for
+//           an x that is not finite
+// (a division an element would be bound by its instructions, not by HBM: 1.29
+// ms for 151,936 x 4,096 bf16), so that code * scale is x within half a step of the 8-bit type (2^-4
 // relative for e4m3 in its normal range). Entries that are not finite do not
 // enter the scale, so they cost their neighbours no precision, and stay
 // visible as NaN in every product that they take part in.
@@ -55,32 +58,64 @@ __device__ __forceinline__ void load8(const T* p, int live, float (&v)[8]) {
   }
 }
 
-// |v| where it is finite, else 0.
-__device__ __forceinline__ float finite_abs(float v) {
-  const float a = fabsf(v);
-  return a <= 3.402823466e+38f ? a : 0.f;
+constexpr float kLargest = 3.402823466e+38f;
+
+// The largest finite |v|, 0 without one.
+__device__ __forceinline__ float largest8(const float (&v)[8]) {
+  float m = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[i]));  // a NaN is passed over
+  if (m > kLargest) {  // an infinity among them
+    m = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[i]) <= kLargest ? fabsf(v[i]) : 0.f);
+  }
+  return m;
+}
+
+// A block's scale, and what its entries are multiplied by.
+struct Scale {
+  float s, inv;
+};
+
+template <bool kE5>
+__device__ __forceinline__ Scale block_scale(float amax) {
+  Scale r;
+  r.s = __fdiv_rn(amax, kE5 ? 57344.f : 448.f);
+  r.s = r.s > 0.f ? r.s : 1.f;
+  r.inv = __frcp_rn(r.s);
+  return r;
 }
 
 template <bool kE5>
-__device__ __forceinline__ float block_scale(float amax) {
-  const float s = __fdiv_rn(amax, kE5 ? 57344.f : 448.f);
-  return s > 0.f ? s : 1.f;
-}
-
-template <bool kE5>
-__device__ __forceinline__ uint32_t code2(float a, float b, float scale) {
-  // inf / scale is inf, and the conversion limits that to +-top: NaN instead
-  a = fabsf(a) <= 3.402823466e+38f ? __fdiv_rn(a, scale) : __int_as_float(0x7fc00000);
-  b = fabsf(b) <= 3.402823466e+38f ? __fdiv_rn(b, scale) : __int_as_float(0x7fc00000);
+__device__ __forceinline__ uint32_t code2(float a, float b) {
   return (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE,
                                             kE5 ? __NV_E5M2 : __NV_E4M3);
 }
 
 template <bool kE5>
-__device__ __forceinline__ uint2 code8(const float (&v)[8], float scale) {
+__device__ __forceinline__ uint2 code8(const float (&v)[8], const Scale& sc) {
+  float y[8];
+  if (sc.s >= 1.17549435e-38f) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = v[i] * sc.inv;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = __fdiv_rn(v[i], sc.s);
+  }
+  // the conversion limits what is too large, infinities included: NaN for those
+  // (inf times a reciprocal is inf; a finite entry gives at most about top)
+  float m = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(y[i]));
+  if (m > kLargest) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (fabsf(y[i]) > kLargest) y[i] = __int_as_float(0x7fc00000);
+  }
   uint2 w;
-  w.x = code2<kE5>(v[0], v[1], scale) | (code2<kE5>(v[2], v[3], scale) << 16);
-  w.y = code2<kE5>(v[4], v[5], scale) | (code2<kE5>(v[6], v[7], scale) << 16);
+  w.x = code2<kE5>(y[0], y[1]) | (code2<kE5>(y[2], y[3]) << 16);
+  w.y = code2<kE5>(y[4], y[5]) | (code2<kE5>(y[6], y[7]) << 16);
   return w;
 }
 
@@ -141,18 +176,15 @@ __global__ void __launch_bounds__(kThreads) rows1_kernel(const QuantArgs a) {
     for (int u = 0; u < kUnroll; ++u) {
       const bool mine = first + u * groups < total;
       float m = 0.f;
-      if (live[u] > 0) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) m = fmaxf(m, finite_abs(v[u][i]));
-      }
+      if (live[u] > 0) m = largest8(v[u]);
       // the 16 lanes of a group agree on `first`, but the two groups of a warp
       // may leave the loop apart: only this group's lanes take part
       const uint32_t lanes = 0xFFFFu << (threadIdx.x & 16);
 #pragma unroll
       for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(lanes, m, o));
       if (!mine) continue;
-      const float s = block_scale<kE5>(m);
-      if (sub == 0) a.scale[row[u] * a.scale_ld + kb[u]] = s;
+      const Scale s = block_scale<kE5>(m);
+      if (sub == 0) a.scale[row[u] * a.scale_ld + kb[u]] = s.s;
       if (live[u] > 0)
         store8(a.q + row[u] * a.q_ld + kb[u] * kBlock + sub * 8, code8<kE5>(v[u], s), live[u],
                a.q_vec);
@@ -190,11 +222,9 @@ __global__ void __launch_bounds__(kThreads) rows128_kernel(const QuantArgs a) {
     load8<T, kVec>(static_cast<const T*>(a.x) + r * a.ld + k, r < a.R ? live : 0, v[i]);
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-#pragma unroll
-    for (int j = 0; j < 8; ++j) m = fmaxf(m, finite_abs(v[i][j]));
-  const float s = block_scale<kE5>(block_max(m, warp_max));
-  if (threadIdx.x == 0) a.scale[rb * a.scale_ld + kb] = s;
+  for (int i = 0; i < 8; ++i) m = fmaxf(m, largest8(v[i]));
+  const Scale s = block_scale<kE5>(block_max(m, warp_max));
+  if (threadIdx.x == 0) a.scale[rb * a.scale_ld + kb] = s.s;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int64_t r = r0 + 16 * i;
@@ -223,45 +253,45 @@ __global__ void __launch_bounds__(kThreads) cols_kernel(const QuantArgs a) {
 #pragma unroll
   for (int i = 0; i < 8; ++i)
     load8<T, kVec>(static_cast<const T*>(a.x) + (k + i) * a.ld + r, k + i < a.K ? live : 0, v[i]);
-  float s[8];
-  if (kSquare) {
+  Scale s[kSquare ? 1 : 8];
+  if constexpr (kSquare) {
     float m = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) m = fmaxf(m, finite_abs(v[i][j]));
+    for (int i = 0; i < 8; ++i) m = fmaxf(m, largest8(v[i]));
     s[0] = block_scale<kE5>(block_max(m, warp_max));
-#pragma unroll
-    for (int j = 1; j < 8; ++j) s[j] = s[0];
-    if (threadIdx.x == 0) a.scale[rb * a.scale_ld + kb] = s[0];
+    if (threadIdx.x == 0) a.scale[rb * a.scale_ld + kb] = s[0].s;
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      float m = 0.f;
+      float w[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) m = fmaxf(m, finite_abs(v[i][j]));
-      row_max[kg][oct * 8 + j] = m;
+      for (int i = 0; i < 8; ++i) w[i] = v[i][j];
+      row_max[kg][oct * 8 + j] = largest8(w);
     }
     __syncthreads();
     if (threadIdx.x < kBlock) {
       float m = 0.f;
 #pragma unroll
       for (int g = 0; g < 16; ++g) m = fmaxf(m, row_max[g][threadIdx.x]);
-      const float sc = block_scale<kE5>(m);
-      row_max[0][threadIdx.x] = sc;
+      const Scale sc = block_scale<kE5>(m);
+      row_max[0][threadIdx.x] = sc.s;
+      row_max[1][threadIdx.x] = sc.inv;
       const int64_t row = rb * kBlock + threadIdx.x;
-      if (row < a.R) a.scale[row * a.scale_ld + kb] = sc;
+      if (row < a.R) a.scale[row * a.scale_ld + kb] = sc.s;
     }
     __syncthreads();
 #pragma unroll
-    for (int j = 0; j < 8; ++j) s[j] = row_max[0][oct * 8 + j];
+    for (int j = 0; j < 8; ++j) {
+      s[j].s = row_max[0][oct * 8 + j];
+      s[j].inv = row_max[1][oct * 8 + j];
+    }
   }
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     float w[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) w[i] = v[i][j];
-    codes[oct * 8 + j][kg ^ oct] = code8<kE5>(w, s[j]);
+    codes[oct * 8 + j][kg ^ oct] = code8<kE5>(w, s[kSquare ? 0 : j]);
   }
   __syncthreads();
   const int64_t kk = kb * kBlock + oct * 8;  // now 16 lanes write a row's 128 codes

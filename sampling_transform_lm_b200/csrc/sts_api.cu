@@ -50,7 +50,8 @@ EncodeTiledFn encode_fn() {
 }
 
 bool map2d(CUtensorMap* m, const void* base, CUtensorMapDataType dt, uint64_t inner, uint64_t outer,
-           uint64_t stride_bytes, uint32_t box_inner, uint32_t box_outer) {
+           uint64_t stride_bytes, uint32_t box_inner, uint32_t box_outer,
+           CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
   EncodeTiledFn enc = encode_fn();
   if (!enc) return false;
   std::memset(m, 0, sizeof(*m));
@@ -59,7 +60,7 @@ bool map2d(CUtensorMap* m, const void* base, CUtensorMapDataType dt, uint64_t in
   const cuuint32_t box[2] = {box_inner, box_outer};
   const cuuint32_t es[2] = {1, 1};
   return enc(m, dt, 2, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -499,8 +500,9 @@ sts_status current_device(int* sms) {
 }
 
 bool tensor_map_2d(CUtensorMap* m, const void* base, CUtensorMapDataType dt, uint64_t inner,
-                   uint64_t outer, uint64_t stride_bytes, uint32_t box_inner, uint32_t box_outer) {
-  return map2d(m, base, dt, inner, outer, stride_bytes, box_inner, box_outer);
+                   uint64_t outer, uint64_t stride_bytes, uint32_t box_inner, uint32_t box_outer,
+                   CUtensorMapSwizzle swizzle) {
+  return map2d(m, base, dt, inner, outer, stride_bytes, box_inner, box_outer, swizzle);
 }
 
 }  // namespace sts

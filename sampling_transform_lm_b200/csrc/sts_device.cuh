@@ -75,6 +75,27 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
   }
 }
 
+// mbar_wait for phases that are due within a fraction of a microsecond: the
+// clock is first read after 64 tries (reading it costs as much as the whole
+// wait), and the limit counts from there.
+__device__ __forceinline__ bool mbar_wait_soon(uint32_t bar, uint32_t parity,
+                                               volatile int* abort_flag, int* err) {
+  uint64_t t0 = 0;
+  for (uint32_t it = 1;; ++it) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((it & 63u) == 0u) {
+      if (*abort_flag) return false;
+      const uint64_t now = global_ns();
+      if (t0 == 0) t0 = now;
+      if (now - t0 > kWaitLimitNs) {
+        *abort_flag = 1;
+        if (err) atomicCAS(err, 0, (int)STS_ERR_TIMEOUT);
+        return false;
+      }
+    }
+  }
+}
+
 // Bounded wait used only on teardown paths: no flag, no error, just a limit.
 __device__ __forceinline__ void mbar_wait_drain(uint32_t bar, uint32_t parity) {
   const uint64_t t0 = global_ns();

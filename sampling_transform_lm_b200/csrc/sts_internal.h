@@ -44,9 +44,10 @@ void launch_end(const LaunchMark& mark, cudaStream_t st);
 sts_status current_device(int* sms);
 
 // A tensor map of a row-major matrix [outer][inner] with rows
-// stride_bytes apart, read in boxes of box_outer rows x 128 bytes, 128-byte swizzle. False on failure.
+// stride_bytes apart, moved in boxes of box_outer rows x box_inner elements. False on failure.
 bool tensor_map_2d(CUtensorMap* m, const void* base, CUtensorMapDataType dt, uint64_t inner,
-                   uint64_t outer, uint64_t stride_bytes, uint32_t box_inner, uint32_t box_outer);
+                   uint64_t outer, uint64_t stride_bytes, uint32_t box_inner, uint32_t box_outer,
+                   CUtensorMapSwizzle swizzle);
 
 // Resolver modes.
 enum ResolveMode : int { kModeForward = 0, kModeSample = 1, kModeFilter = 2 };

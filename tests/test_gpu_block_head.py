@@ -20,7 +20,7 @@ def _expand(scale, R, K, block_rows):
 
 
 def quantize_reference(x, block_rows, dtype):
-    """The documented formula with the CPU's IEEE fp32 division and 8-bit conversion."""
+    """The documented formula with the CPU's IEEE fp32 arithmetic and 8-bit conversion."""
     R, K = x.shape
     x = x.float().cpu()
     Rb, Kb = -(-R // block_rows), -(-K // 128)
@@ -30,7 +30,9 @@ def quantize_reference(x, block_rows, dtype):
     finite = torch.isfinite(b)
     scale = torch.where(finite, b.abs(), 0.0).amax((1, 3)) / TOP[dtype]
     scale = torch.where(scale > 0, scale, 1.0)
-    q = torch.where(finite, (b / scale[:, None, :, None]).clamp(-TOP[dtype], TOP[dtype]), math.nan)
+    s = scale[:, None, :, None]
+    y = torch.where(s >= 2.0 ** -126, b * (1.0 / s), b / s)
+    q = torch.where(finite, y.clamp(-TOP[dtype], TOP[dtype]), math.nan)
     return q.reshape(Rb * block_rows, Kb * 128)[:R, :K].to(dtype), scale
 
 
