@@ -14,13 +14,17 @@
 //
 // One pass over the row in each direction; HBM bounds both. The forward's
 // running sums are taken against a fixed base b instead of a running maximum:
-//   x_i = c (z_i - b),  c = log2(e) / tau,  S' = sum 2^x_i,  S'_1 = sum 2^x_i x_i
-// Any base gives the same quotients, so b is the maximum of the first 4,096 to
-// 8,192 elements and moves only when an element exceeds it by 2^64: the inner
-// loop is a difference, a product, a clamp, an exponential and two sums an
-// element (differences of logits: no temperature overflows them). The
-// clamp at -200 (2^-200 is 0 in fp32) keeps 0 * inf out of S'_1 for masked
-// logits. Each thread's sums (fp32, about V / 256 terms) are joined in float64.
+//   x_i = c z_i - b,  c = log2(e) / tau,  S' = sum 2^x_i,  S'_1 = sum 2^x_i x_i
+// Any base gives the same quotients, so b is c times the maximum of the first
+// chunk of 2,048 to 8,192 elements and moves, a thread at a time, only when an
+// element exceeds it by more than a factor of 2 (a larger x would carry a larger
+// rounding into the terms that matter). An element costs a clamp, two FMAs (c
+// in two parts: the rounding of one would be a common factor of all x), an
+// exponential and two sums. The clamp keeps x at -200 or above (2^-200 is 0 in
+// fp32), so that masked logits put no 0 * inf into S'_1. Each thread's sums
+// (fp32, two of each) are joined in float64. Rows whose largest c z_i leaves
+// fp32's exact range, 2^20 (nothing but masks of the type's lowest value, say),
+// form x from differences of logits instead.
 //
 // The alternatives ride in the same loop: a lower bound of the n-th largest
 // element (the n-th largest of group maxima of the first chunk, tightened as
@@ -35,6 +39,7 @@
 // vocabulary; the first block joins their results over distributed shared
 // memory. One launch, no workspace, nothing shared between calls.
 #include <cmath>
+#include <type_traits>
 
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
@@ -47,19 +52,20 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256;     // of the gradient, and of the forward for long rows
 constexpr int kUnroll = 4;       // 16-byte loads in flight per thread
 constexpr int kMaxTop = 64;      // alternatives per row
 constexpr int kMaxGiven = 512;   // given tokens per row
 constexpr int kMaxParts = 8;     // portable cluster size
 constexpr int kKeyCap = 1024;    // keys kept between two tightenings
+constexpr int64_t kShortRow = 16384;  // rows up to this have blocks of 128 threads
 constexpr double kLog2eD = 1.4426950408889634074;
 constexpr double kLn2 = 0.69314718055994530942;
 constexpr float kNegInf = -INFINITY;
 
 // log2(e) / tau, finite for every tau > 0
-__device__ __forceinline__ float exponent_scale(float tau) {
-  return (float)fmin(kLog2eD / (double)tau, 3.402823466e+38);
+__device__ __forceinline__ double exponent_scale(float tau) {
+  return fmin(kLog2eD / (double)tau, 3.402823466e+38);
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -88,8 +94,22 @@ struct Vec {
   static constexpr int kN = 16 / (int)sizeof(T);
   uint4 w;
   __device__ __forceinline__ void load(const T* p) { w = __ldg(reinterpret_cast<const uint4*>(p)); }
+  __device__ __forceinline__ void none() {  // all -inf
+    constexpr uint32_t k = std::is_same<T, float>::value           ? 0xFF800000u
+                           : std::is_same<T, __nv_bfloat16>::value ? 0xFF80FF80u
+                                                                   : 0xFC00FC00u;
+    w = make_uint4(k, k, k, k);
+  }
   __device__ __forceinline__ void f32(float (&v)[kN]) const;
   __device__ __forceinline__ float largest() const;  // NaN where one is NaN
+  __device__ __forceinline__ float at(int k) const {  // one element, chosen at run time
+    constexpr int kPer = 4 / (int)sizeof(T);
+    const int i = k / kPer;
+    const uint32_t u = i == 0 ? w.x : i == 1 ? w.y : i == 2 ? w.z : w.w;
+    if constexpr (kPer == 1) return __uint_as_float(u);
+    const uint16_t h = (uint16_t)(u >> ((k & 1) * 16));
+    return to_f32(*reinterpret_cast<const T*>(&h));
+  }
 };
 
 template <>
@@ -169,85 +189,137 @@ struct FwdArgs {
 
 struct Share {  // what one block found in its stretch
   double s0, s1;
-  float base;
+  double e;  // the exponent of their base
   int bad;
   int found;
-  int pad;
 };
 
+template <int kT>
 struct FwdSmem {
   uint64_t keys[kKeyCap];
   uint64_t top[kMaxTop];
-  uint64_t joined[kMaxParts * kMaxTop];
-  Share share;
-  float group_max[kThreads];
-  double red0[kThreads / 32], red1[kThreads / 32];
-  float redb[kThreads / 32];
-  float cut;
+  uint64_t lists[kMaxParts][kMaxTop];
+  Share share[kMaxParts];  // [0]: this block's; all of them in the joining block
+  float group_max[kT];
+  double red0[kT / 32], red1[kT / 32];
+  double rede[kT / 32];
+  float cut, chunk_max, log_sum;
   uint32_t count;
   uint32_t hist[256];
   uint32_t digit, above;
-  uint32_t ties[kThreads / 32];
+  uint32_t ties[kT / 32];
 };
 
 // The n largest of keys[0, c) (all different), in descending order, to out.
 // Every thread of the block takes part; barriers before and after are the
-// caller's. c^2 / 256 comparisons a thread: c is a few n, at most kKeyCap.
+// caller's. Each key counts those above it; several lanes share a key where
+// there are fewer keys than threads.
+template <int kT>
 __device__ __forceinline__ void rank_keys(const uint64_t* keys, int c, int n, uint64_t* out) {
-  for (int i = threadIdx.x; i < c; i += kThreads) {
-    const uint64_t k = keys[i];
+  int share = 1;
+  while (share < 32 && c * share * 2 <= kT) share *= 2;
+  const int sub = (int)threadIdx.x & (share - 1);
+  for (int i0 = 0; i0 < c; i0 += kT / share) {
+    const int i = i0 + (int)threadIdx.x / share;
+    const uint64_t k = i < c ? keys[i] : ~0ull;
     int above = 0;
-    for (int j = 0; j < c; ++j) above += keys[j] > k ? 1 : 0;
-    if (above < n) out[above] = k;
+#pragma unroll 4
+    for (int j = sub; j < c; j += share) above += keys[j] > k ? 1 : 0;
+    for (int o = 1; o < share; o *= 2) above += __shfl_xor_sync(0xFFFFFFFFu, above, o);
+    if (i < c && sub == 0 && above < n) out[above] = k;
   }
 }
 
-// One thread's running sums against its base (a logit).
+// c = log2(e) / tau in two parts, and whether the thread's base is far: x = c (z - base)
+struct Factor {
+  float hi, lo;
+  bool far;
+};
+
+// One thread's running sums against its base (a logit), in two halves.
 struct Sums {
-  float s0, s1, base;
+  float s0[2], s1[2];
+  float base;   // x = 0 there
+  float b;      // c base, rounded once: what the sums are really against
+  float least;  // logits below it count as this one
 };
 constexpr float kLowest = -3.402823466e+38f;  // the base before anything was seen
+constexpr float kFar = 1048576.f;  // c base beyond it: far (its rounding would be an exponent's size)
 
-__device__ __forceinline__ void rebase(Sums& s, float to, float c) {
-  const float by = (s.base - to) * c;  // 0 or less, -inf from kLowest
+// The exponent of the sums' base, exactly: x = c z - this (far: c (z - base)).
+__device__ __forceinline__ double base_exponent(const Sums& s, bool far, double c) {
+  return far ? __dmul_rn(c, (double)s.base) : (double)s.b;
+}
+
+__device__ __forceinline__ void shift(Sums& s, float to, float b, float by, const Factor& c) {
   const float f = ex2(fmaxf(by, -200.f));
-  s.s1 = f == 0.f ? 0.f : fmaf(by, s.s0, s.s1) * f;
-  s.s0 *= f;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    s.s1[h] = f == 0.f ? 0.f : fmaf(by, s.s0[h], s.s1[h]) * f;
+    s.s0[h] *= f;
+  }
   s.base = to;
+  s.b = b;
+  s.least = fmaxf(to - 200.f / c.hi, kLowest);
 }
 
-__device__ __forceinline__ void add(Sums& s, float z, float c) {
-  const float x = fmaxf((z - s.base) * c, -200.f);
+// Moves the base (upwards; the sums are 0 where it is kLowest), and the thread
+// between the near and the far form as the new base has it.
+__device__ __forceinline__ void rebase(Sums& s, float to, Factor& c) {
+  const float b = to * c.hi;
+  const bool far = !(fabsf(b) < kFar) || !(200.f / c.hi < 1e30f);
+  float by;  // the old base's exponent over the new one's: 0 or less
+  if (far)
+    by = c.far ? (s.base - to) * c.hi : -fmaf(to, c.lo, fmaf(to, c.hi, -s.b));
+  else
+    by = c.far ? fmaf(s.base, c.lo, fmaf(s.base, c.hi, -b)) : s.b - b;
+  shift(s, to, b, by, c);
+  c.far = far;
+}
+
+template <bool kFarForm>
+__device__ __forceinline__ void add(Sums& s, int h, float z, const Factor& c) {
+  float x;
+  if (kFarForm) {
+    const float d = z - s.base;
+    // (a masked logit may give NaN here, -inf times both parts of c: fmaxf drops it)
+    x = fmaxf(fmaf(d, c.lo, d * c.hi), -200.f);
+  } else {
+    const float y = fmaxf(z, s.least);
+    x = fmaf(y, c.lo, fmaf(y, c.hi, -s.b));
+  }
   const float e = ex2(x);
-  s.s0 += e;
-  s.s1 = fmaf(e, x, s.s1);
+  s.s0[h] += e;
+  s.s1[h] = fmaf(e, x, s.s1[h]);
 }
 
-__device__ __forceinline__ void keep(FwdSmem& sm, float z, uint32_t id) {
+template <int kT>
+__device__ __forceinline__ void keep(FwdSmem<kT>& sm, float z, uint32_t id) {
   const uint32_t at = atomicAdd(&sm.count, 1u);
   if (at < (uint32_t)kKeyCap) sm.keys[at] = token_key(z, id);
 }
 
 // An element on its own (a head, a tail, or one of a vector above the bound):
 // keep it where it is above `cut`, and move the base where it must.
-__device__ __forceinline__ void consider(FwdSmem& sm, Sums& s, float z, float c, uint32_t id,
-                                         float cut, bool or_equal) {
+template <int kT>
+__device__ __forceinline__ void consider(FwdSmem<kT>& sm, Sums& s, float z, Factor& c,
+                                         uint32_t id, float cut, bool or_equal) {
   if (z > cut || (or_equal && z == cut && z > kNegInf)) keep(sm, z, id);
-  if ((z - s.base) * c > 64.f && z < INFINITY) rebase(s, z, c);
+  if ((z - s.base) * c.hi > 1.f && z < INFINITY) rebase(s, z, c);
 }
 
 // The n largest of the stretch, digit by digit, for rows whose keys did not
 // fit: four histograms fix the n-th largest logit, then everything above it is
 // collected, and the ties at it in order of their ids.
-template <typename T>
-__device__ __noinline__ int search_again(FwdSmem& sm, const T* z, int len, uint32_t id0, int n) {
+template <typename T, int kT>
+__device__ __noinline__ int search_again(FwdSmem<kT>& sm, const T* z, int len, uint32_t id0, int n) {
   uint32_t prefix = 0, want = (uint32_t)n;
   for (int shift = 24; shift >= 0; shift -= 8) {
     __syncthreads();
-    sm.hist[threadIdx.x] = 0;
+    for (int i = threadIdx.x; i < 256; i += kT) sm.hist[i] = 0;
     __syncthreads();
     const uint32_t mask = shift == 24 ? 0u : 0xFFFFFFFFu << (shift + 8);
-    for (int i = threadIdx.x; i < (len + 31) / 32 * 32; i += kThreads) {
+    for (int i = threadIdx.x; i < (len + 31) / 32 * 32; i += kT) {
       bool in = false;
       uint32_t digit = 0;
       if (i < len) {
@@ -280,7 +352,7 @@ __device__ __noinline__ int search_again(FwdSmem& sm, const T* z, int len, uint3
   if (threadIdx.x == 0) sm.count = 0;
   __syncthreads();
   uint32_t ties = 0;
-  for (int i0 = 0; i0 < len; i0 += kThreads) {
+  for (int i0 = 0; i0 < len; i0 += kT) {
     const int i = i0 + (int)threadIdx.x;
     bool tie = false;
     float v = kNegInf;
@@ -295,7 +367,7 @@ __device__ __noinline__ int search_again(FwdSmem& sm, const T* z, int len, uint3
       if ((threadIdx.x & 31) == 0) sm.ties[threadIdx.x >> 5] = (uint32_t)__popc(ballot);
       __syncthreads();
       uint32_t before = ties, all = ties;
-      for (int w = 0; w < kThreads / 32; ++w) {
+      for (int w = 0; w < kT / 32; ++w) {
         if (w < (int)(threadIdx.x >> 5)) before += sm.ties[w];
         all += sm.ties[w];
       }
@@ -309,9 +381,39 @@ __device__ __noinline__ int search_again(FwdSmem& sm, const T* z, int len, uint3
   return (int)min(sm.count, (uint32_t)kKeyCap);
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads) forward_kernel(const FwdArgs a) {
-  __shared__ FwdSmem sm;
+// The first bound, from one chunk (vm: the maxima of this thread's vectors):
+// sm.cut is the n-th largest of `groups` group maxima, and sm.chunk_max the
+// largest; -inf where fewer than n groups hold anything. NaN counts as nothing.
+template <int kT>
+__device__ __forceinline__ void first_bound(FwdSmem<kT>& sm, const float (&vm)[kUnroll], int groups,
+                                            int n) {
+  const int tid = threadIdx.x;
+  const int per_group = kT / groups;
+  float m = fmaxf(fmaxf(vm[0], vm[1]), fmaxf(vm[2], vm[3]));
+  for (int o = 1; o < per_group; o *= 2) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+  if ((tid & (per_group - 1)) == 0) sm.group_max[tid / per_group] = m;
+  if (tid == 0) sm.cut = kNegInf;
+  __syncthreads();
+  // per_group lanes share a group's count of those above it
+  const int mine = tid / per_group, sub = tid & (per_group - 1);
+  const float v = sm.group_max[mine];
+  int above = 0;
+#pragma unroll 4
+  for (int j = sub; j < groups; j += per_group) {
+    const float o = sm.group_max[j];
+    above += (o > v || (o == v && j < mine)) ? 1 : 0;
+  }
+  for (int o = 1; o < per_group; o *= 2) above += __shfl_xor_sync(0xFFFFFFFFu, above, o);
+  if (v > kNegInf && sub == 0) {
+    if (above == n - 1) sm.cut = v;
+    if (above == 0) sm.chunk_max = v;
+  }
+  __syncthreads();
+}
+
+template <typename T, int kT>
+__global__ void __launch_bounds__(kT, 1024 / kT) forward_kernel(const FwdArgs a) {
+  __shared__ FwdSmem<kT> sm;
   constexpr int kN = Vec<T>::kN;
   const int parts = a.parts;
   const int64_t row = (int64_t)blockIdx.x / parts;
@@ -320,7 +422,11 @@ __global__ void __launch_bounds__(kThreads) forward_kernel(const FwdArgs a) {
   const int n = max(a.n, 1);  // the first alternative gives the maximum
   const float tau = a.tau ? a.tau[row] : 1.f;
   const bool tau_ok = tau > 0.f && tau < INFINITY;
-  const float c = exponent_scale(tau_ok ? tau : 1.f);
+  const double cd = exponent_scale(tau_ok ? tau : 1.f);
+  Factor c;
+  c.hi = (float)cd;
+  c.lo = (float)(cd - (double)c.hi);
+  c.far = true;  // until a maximum shows that it is not
 
   const int v0 = (int)min((int64_t)part * a.stretch, (int64_t)a.V);
   const int len = min(a.stretch, a.V - v0);
@@ -334,63 +440,52 @@ __global__ void __launch_bounds__(kThreads) forward_kernel(const FwdArgs a) {
 
   if (tid == 0) sm.count = 0;
 
-  Sums s{0.f, 0.f, kLowest};
+  Sums s{{0.f, 0.f}, {0.f, 0.f}, kLowest, 0.f, kLowest};
   float cut = kNegInf;   // nothing at or below it can be an alternative any more
-  float seen = kNegInf;  // only to catch NaN: the maximum of everything, NaN if any is
-  int groups = 32;       // group maxima for the first bound: at least n
-  while (groups < 4 * n && groups < kThreads) groups *= 2;
-  const int per_group = kThreads / groups;
+  float seen = kNegInf;  // only to catch NaN and inf: the maximum of what was looked at closely
+  int groups = 32;       // group maxima for the first bound: 2 n at least
+  while (groups < 2 * n && groups < kT) groups *= 2;
 
   bool bound = false;  // a finite bound has been found (the same in every thread)
-  int next_tighten = 4;
-  for (int it = 0, i0 = 0; i0 < body || it == 0; ++it, i0 += kThreads * kUnroll) {
+  // the keys are about n by the first chunk, n more for each doubling of the row
+  int next_tighten = n > 16 ? 2 : 4;
+  for (int it = 0, i0 = 0; i0 < body || it == 0; ++it, i0 += kT * kUnroll) {
     Vec<T> v[kUnroll];
     float vm[kUnroll];
+    if (i0 + kT * kUnroll <= body) {
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int i = i0 + u * kThreads + tid;
-      if (i < body) v[u].load(zb + (int64_t)i * kN);
+      for (int u = 0; u < kUnroll; ++u) v[u].load(zb + (int64_t)(i0 + u * kT + tid) * kN);
+    } else {
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        const int i = i0 + u * kT + tid;
+        if (i < body)
+          v[u].load(zb + (int64_t)i * kN);
+        else
+          v[u].none();
+      }
     }
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int i = i0 + u * kThreads + tid;
-      vm[u] = i < body ? v[u].largest() : kNegInf;
-    }
+    for (int u = 0; u < kUnroll; ++u) vm[u] = v[u].largest();
     bool equal = false;  // whether ties with the bound still count
     if (!bound) {
-      float m = max_nan(max_nan(vm[0], vm[1]), max_nan(vm[2], vm[3]));
-      for (int o = 1; o < per_group; o *= 2) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-      if (tid % per_group == 0) sm.group_max[tid / per_group] = m;
-      if (tid == 0) sm.cut = kNegInf;
-      __syncthreads();
-      if (tid < groups) {  // the n-th largest group maximum (NaN and -inf count as least)
-        const float mine = sm.group_max[tid];
-        if (mine > kNegInf) {
-          int above = 0;
-          for (int j = 0; j < groups; ++j) {
-            const float o = sm.group_max[j];
-            above += (o > mine || (o == mine && j < tid)) ? 1 : 0;
-          }
-          if (above == n - 1) sm.cut = mine;
-          if (above == 0) sm.redb[0] = mine;
-        }
-      }
-      __syncthreads();
+      first_bound(sm, vm, groups, n);
       if (sm.cut > kNegInf) {
         bound = true;
         equal = true;  // the n elements of the bound are of this very chunk
         cut = sm.cut;
-        const float to = fminf(sm.redb[0], 3.402823466e+38f);  // the base: the chunk's maximum
-        if (to > s.base) rebase(s, to, c);
+        // the base: the chunk's maximum
+        const float to = fmaxf(fminf(sm.chunk_max, -kLowest), s.base);
+        rebase(s, to, c);
       }
-      __syncthreads();  // group_max, cut and redb are free again
+      __syncthreads();  // group_max, cut and chunk_max are free again
     } else if (it >= next_tighten && a.n > 1) {
-      next_tighten *= 4;
+      next_tighten *= n > 16 ? 2 : 4;
       __syncthreads();
       const int cnt = (int)min(sm.count, (uint32_t)kKeyCap);
       const bool whole = sm.count <= (uint32_t)kKeyCap;
-      if (whole && cnt >= n) {
-        rank_keys(sm.keys, cnt, n, sm.top);
+      if (whole && cnt > n) {
+        rank_keys<kT>(sm.keys, cnt, n, sm.top);
         __syncthreads();
         if (tid < n) sm.keys[tid] = sm.top[tid];
         if (tid == 0) sm.count = (uint32_t)n;
@@ -398,47 +493,86 @@ __global__ void __launch_bounds__(kThreads) forward_kernel(const FwdArgs a) {
       }
       __syncthreads();
     }
+    // vectors with something above the bound, a NaN, or before any bound: looked
+    // at element by element, before their sums, in one rolled loop (rare: about
+    // n elements for each doubling of the row)
+    uint32_t look = 0;
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int i = i0 + u * kThreads + tid;
-      if (i < body) {
+    for (int u = 0; u < kUnroll; ++u)
+      look |= (equal ? !(vm[u] < cut) : !(vm[u] <= cut) || (!bound && vm[u] > kNegInf)) ? 1u << u : 0u;
+    while (look != 0u) {
+      const int u = __ffs((int)look) - 1;
+      look &= look - 1u;
+      Vec<T> x = v[0];
+#pragma unroll
+      for (int i = 1; i < kUnroll; ++i)
+        if (u == i) x = v[i];
+      const uint32_t id = (uint32_t)(v0 + head + (i0 + u * kT + tid) * kN);
+      float f[kN];
+      x.f32(f);
+      uint32_t which = 0;  // its elements above the bound, and NaN
+#pragma unroll
+      for (int k = 0; k < kN; ++k)
+        which |= (equal ? !(f[k] < cut) : !(f[k] <= cut)) ? 1u << k : 0u;
+      while (which != 0u) {
+        const int k = __ffs((int)which) - 1;
+        which &= which - 1u;
+        const float y = x.at(k);
+        seen = max_nan(seen, y);
+        consider(sm, s, y, c, id + (uint32_t)k, cut, equal);
+      }
+    }
+    __syncwarp();  // or the lanes that looked would run the rest of the row on their own
+    if (!c.far) {
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
         float f[kN];
         v[u].f32(f);
-        // also taken for NaN, and where no bound is known yet
-        if (!(vm[u] < cut) && (equal || !(vm[u] <= cut) || cut == kNegInf)) {
-          seen = max_nan(seen, vm[u]);
-          const uint32_t id = (uint32_t)(v0 + head + i * kN);
 #pragma unroll
-          for (int k = 0; k < kN; ++k) consider(sm, s, f[k], c, id + (uint32_t)k, cut, equal);
+        for (int k = 0; k < kN; ++k) add<false>(s, k & 1, f[k], c);
+      }
+    } else {
+      for (int u = 0; u < kUnroll; ++u) {
+#pragma unroll 1
+        for (int k = 0; k < kN; ++k) {
+          Vec<T> x = v[0];
+#pragma unroll
+          for (int i = 1; i < kUnroll; ++i)
+            if (u == i) x = v[i];
+          add<true>(s, 0, x.at(k), c);
         }
-#pragma unroll
-        for (int k = 0; k < kN; ++k) add(s, f[k], c);
       }
     }
   }
   // the elements outside the vectors: ids below (head) or above (tail) all others
-  for (int i = tid; i < head + (len - tail0); i += kThreads) {
+  for (int i = tid; i < head + (len - tail0); i += kT) {
     const int at = i < head ? i : tail0 + (i - head);
     const float f = to_f32(z[at]);
     seen = max_nan(seen, f);
     consider(sm, s, f, c, (uint32_t)(v0 + at), cut, true);
-    add(s, f, c);
+    if (c.far)
+      add<true>(s, 0, f, c);
+    else
+      add<false>(s, 0, f, c);
   }
 
   // ---- join the block's sums (float64) and find its n largest
   {
-    float top_base = s.base;
+    const double own = base_exponent(s, c.far, cd);
+    double e = own;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-      top_base = fmaxf(top_base, __shfl_xor_sync(0xFFFFFFFFu, top_base, o));
+    for (int o = 16; o > 0; o >>= 1) e = fmax(e, __shfl_xor_sync(0xFFFFFFFFu, e, o));
+    if ((tid & 31) == 0) sm.rede[tid >> 5] = e;
     __syncthreads();
-    if ((tid & 31) == 0) sm.redb[tid >> 5] = top_base;
-    __syncthreads();
-    for (int w = 0; w < kThreads / 32; ++w) top_base = fmaxf(top_base, sm.redb[w]);
-    const double by = ((double)s.base - (double)top_base) * (double)c;
-    const double f = by < -300.0 ? 0.0 : exp2(by);
-    double s0 = (double)s.s0 * f;
-    double s1 = f == 0.0 ? 0.0 : ((double)s.s1 + by * (double)s.s0) * f;
+#pragma unroll
+    for (int w = 0; w < kT / 32; ++w) e = fmax(e, sm.rede[w]);
+    double s0 = (double)s.s0[0] + (double)s.s0[1], s1 = (double)s.s1[0] + (double)s.s1[1];
+    if (own != e) {
+      const double by = own - e;
+      const double f = by < -300.0 ? 0.0 : exp2(by);
+      s1 = f == 0.0 ? 0.0 : (s1 + by * s0) * f;
+      s0 *= f;
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
       s0 += __shfl_xor_sync(0xFFFFFFFFu, s0, o);
@@ -451,74 +585,91 @@ __global__ void __launch_bounds__(kThreads) forward_kernel(const FwdArgs a) {
     const int bad = __syncthreads_or(seen != seen || seen == INFINITY);
     if (tid == 0) {
       s0 = s1 = 0.0;
-      for (int w = 0; w < kThreads / 32; ++w) {
+      for (int w = 0; w < kT / 32; ++w) {
         s0 += sm.red0[w];
         s1 += sm.red1[w];
       }
-      sm.share.s0 = s0;
-      sm.share.s1 = s1;
-      sm.share.base = top_base;
-      sm.share.bad = bad;
+      sm.share[0].s0 = s0;
+      sm.share[0].s1 = s1;
+      sm.share[0].e = e;
+      sm.share[0].bad = bad;
     }
   }
   int cnt = (int)min(sm.count, (uint32_t)kKeyCap);
-  if (sm.count > (uint32_t)kKeyCap) {  // the same in every thread: a barrier has passed
-    cnt = search_again<T>(sm, z, len, (uint32_t)v0, n);
-  }
-  rank_keys(sm.keys, cnt, n, sm.top);
-  if (tid == 0) sm.share.found = min(cnt, n);
+  if (sm.count > (uint32_t)kKeyCap)  // the same in every thread: a barrier has passed
+    cnt = search_again<T, kT>(sm, z, len, (uint32_t)v0, n);
+  rank_keys<kT>(sm.keys, cnt, n, sm.top);
+  if (tid == 0) sm.share[0].found = min(cnt, n);
 
   // ---- join the cluster's blocks
   int found;
   double s0, s1;
-  float base;
+  double e;
   int bad;
-  const uint64_t* top = sm.top;
   if (parts > 1) {
     cg::cluster_group cluster = cg::this_cluster();
     cluster.sync();
     if (part == 0) {
-      for (int i = tid; i < parts * kMaxTop; i += kThreads) {
-        const int p = i / kMaxTop, j = i % kMaxTop;
-        const FwdSmem* other = cluster.map_shared_rank(&sm, p);
-        // absent ones get keys below every real one, all different
-        sm.joined[i] = j < other->share.found ? other->top[j] : (uint64_t)i;
+      for (int i = tid; i < parts * n; i += kT) {
+        const int p = i / n, j = i - p * n;
+        sm.lists[p][j] = cluster.map_shared_rank(&sm, p)->top[j];
       }
-      base = kNegInf;
-      for (int p = 0; p < parts; ++p)
-        base = fmaxf(base, cluster.map_shared_rank(&sm, p)->share.base);
-      s0 = s1 = 0.0;
-      bad = 0;
-      found = 0;
-      for (int p = 0; p < parts; ++p) {
-        const Share sh = cluster.map_shared_rank(&sm, p)->share;
-        const double by = ((double)sh.base - (double)base) * (double)c;
-        const double f = by < -300.0 ? 0.0 : exp2(by);
-        s0 += sh.s0 * f;
-        s1 += f == 0.0 ? 0.0 : (sh.s1 + by * sh.s0) * f;
-        bad |= sh.bad;
-        found += sh.found;
-      }
-      found = min(found, n);
+      if (tid > 0 && tid < parts) sm.share[tid] = cluster.map_shared_rank(&sm, tid)->share[0];
     }
     cluster.sync();  // the others' shared memory is no longer read
     if (part != 0) return;
-    rank_keys(sm.joined, parts * kMaxTop, n, sm.top);
+    e = sm.share[0].e;
+    for (int p = 1; p < parts; ++p) e = fmax(e, sm.share[p].e);
+    s0 = s1 = 0.0;
+    bad = 0;
+    found = 0;
+    for (int p = 0; p < parts; ++p) {
+      const Share sh = sm.share[p];
+      const double by = sh.e - e;
+      const double f = by < -300.0 ? 0.0 : exp2(by);
+      s0 += sh.s0 * f;
+      s1 += f == 0.0 ? 0.0 : (sh.s1 + by * sh.s0) * f;
+      bad |= sh.bad;
+      found += sh.found;
+    }
+    found = min(found, n);
+    // each list is in order: a key's place is its own and, in every other list,
+    // the number of keys above it
+    for (int i = tid; i < parts * n; i += kT) {
+      const int p = i / n, j = i - p * n;
+      if (j >= sm.share[p].found) continue;
+      const uint64_t k = sm.lists[p][j];
+      int above = j;
+      for (int q = 0; q < parts && above < n; ++q) {
+        if (q == p) continue;
+        int lo_ = 0, hi_ = sm.share[q].found;
+        while (lo_ < hi_) {
+          const int mid = (lo_ + hi_) >> 1;
+          if (sm.lists[q][mid] > k)
+            lo_ = mid + 1;
+          else
+            hi_ = mid;
+        }
+        above += lo_;
+      }
+      if (above < n) sm.top[above] = k;
+    }
     __syncthreads();
   } else {
     __syncthreads();
-    found = sm.share.found;
-    s0 = sm.share.s0;
-    s1 = sm.share.s1;
-    base = sm.share.base;
-    bad = sm.share.bad;
+    found = sm.share[0].found;
+    s0 = sm.share[0].s0;
+    s1 = sm.share[0].s1;
+    e = sm.share[0].e;
+    bad = sm.share[0].bad;
   }
+  const uint64_t* top = sm.top;
 
-  // ---- the row's results
+  // ---- the row's results: the sums' logarithm and the rest by one warp
   int reason = (tau_ok ? 0 : STS_ROW_BAD_TEMPERATURE) | (bad ? STS_ROW_BAD_LOGIT : 0);
   {
     int out = 0;
-    for (int j = tid; j < a.m; j += kThreads) {
+    for (int j = tid; j < a.m; j += kT) {
       const int64_t y = a.tokens[row * a.tokens_ld + j];
       out |= (y < -1 || y >= a.V) ? 1 : 0;
     }
@@ -527,25 +678,29 @@ __global__ void __launch_bounds__(kThreads) forward_kernel(const FwdArgs a) {
   const float nan = __int_as_float(0x7fc00000);
   const bool empty = reason == 0 && found == 0;
   const float zmax = found > 0 ? key_logit(top[0]) : kNegInf;
-  // S = sum 2^(c (z - zmax)); by: what the base is off zmax
-  const double by = found > 0 ? ((double)base - (double)zmax) * (double)c : 0.0;
-  const double total = s0 * exp2(by);
-  const double ln_total = log(total);
-  const float log_sum = reason ? nan : empty ? kNegInf : (float)ln_total;
-  if (tid == 0) {
-    if (a.logit_max) a.logit_max[row] = reason ? nan : zmax;
-    if (a.log_sum) a.log_sum[row] = log_sum;
-    if (a.lse)
-      a.lse[row] = reason ? nan : empty ? kNegInf : (float)((double)zmax / (double)tau + ln_total);
-    if (a.entropy) {
-      const double h = ln_total - kLn2 * (s1 / s0 + by);
-      a.entropy[row] = reason ? nan : empty ? 0.f : (float)fmax(h, 0.0);
+  if (tid < 32) {
+    // S = sum 2^(c (z - zmax)); by: what the sums' base is off that
+    const double by = found > 0 ? e - __dmul_rn(cd, (double)zmax) : 0.0;
+    const double ln_total = log(s0 * exp2(by));
+    const float log_sum = reason ? nan : empty ? kNegInf : (float)ln_total;
+    if (tid == 0) {
+      sm.log_sum = log_sum;
+      if (a.logit_max) a.logit_max[row] = reason ? nan : zmax;
+      if (a.log_sum) a.log_sum[row] = log_sum;
+      if (a.lse)
+        a.lse[row] = reason ? nan : empty ? kNegInf : (float)((double)zmax / (double)tau + ln_total);
+      if (a.entropy) {
+        const double h = ln_total - kLn2 * (s1 / s0 + by);
+        a.entropy[row] = reason ? nan : empty ? 0.f : (float)fmax(h, 0.0);
+      }
+      if (a.flags)
+        a.flags[row] = reason ? (STS_ROW_INVALID | reason) : empty ? STS_ROW_EMPTY : 0;
     }
-    if (a.flags)
-      a.flags[row] = reason ? (STS_ROW_INVALID | reason) : empty ? STS_ROW_EMPTY : 0;
   }
+  __syncthreads();
+  const float log_sum = sm.log_sum;
   const T* zrow = static_cast<const T*>(a.z) + row * a.ld;
-  for (int j = tid; j < a.m; j += kThreads) {
+  for (int j = tid; j < a.m; j += kT) {
     const int64_t y = a.tokens[row * a.tokens_ld + j];
     float lp = nan;
     if (!reason) {
@@ -558,7 +713,7 @@ __global__ void __launch_bounds__(kThreads) forward_kernel(const FwdArgs a) {
     }
     a.logprob[row * a.m + j] = lp;
   }
-  for (int j = tid; j < a.n; j += kThreads) {
+  for (int j = tid; j < a.n; j += kT) {
     const bool has = !reason && j < found;
     a.top_id[row * a.n + j] = has ? (int64_t)key_id(top[j]) : -1;
     a.top_logprob[row * a.n + j] =
@@ -612,12 +767,13 @@ __device__ __forceinline__ void store_vec(O* p, const float (&v)[kN]) {
 }
 
 struct RowCoef {
-  float zmax, c, l2s;  // x = (z - zmax) c - l2s, p = 2^x
-  float a, b;          // dz = p (a + b x)
+  float zmax, c, lo, l2s;  // x = (z - zmax) (c + lo) - l2s, p = 2^x
+  float a, b;              // dz = p (a + b x)
 };
 
 __device__ __forceinline__ float grad_of(float z, const RowCoef& k) {
-  const float x = fmaxf(fmaf(z - k.zmax, k.c, -k.l2s), -200.f);
+  const float d = fmaxf(z - k.zmax, kLowest);  // -inf - zmax: no 0 * inf below
+  const float x = fmaxf(fmaf(d, k.c, fmaf(d, k.lo, -k.l2s)), -200.f);
   return ex2(x) * fmaf(k.b, x, k.a);
 }
 
@@ -672,13 +828,15 @@ __global__ void __launch_bounds__(kThreads) backward_kernel(const BwdArgs a) {
   sum = 0.0;
   for (int w = 0; w < kThreads / 32; ++w) sum += sm.part[w];
 
-  RowCoef k{0.f, 0.f, 0.f, 0.f, 0.f};
+  RowCoef k{0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   float tau = 1.f;
   if (live) {
     tau = a.tau ? a.tau[row] : 1.f;
     const double h = a.grad_entropy ? (double)a.grad_entropy[row] : 0.0;
     k.zmax = a.logit_max[row];
-    k.c = exponent_scale(tau);
+    const double cd = exponent_scale(tau);
+    k.c = (float)cd;
+    k.lo = (float)(cd - (double)k.c);
     k.l2s = (float)((double)a.log_sum[row] * kLog2eD);
     k.a = (float)(-(sum + (h != 0.0 ? h * (double)a.entropy[row] : 0.0)) / (double)tau);
     k.b = (float)(-h * kLn2 / (double)tau);
@@ -751,18 +909,18 @@ __global__ void __launch_bounds__(kThreads) backward_kernel(const BwdArgs a) {
 
 // Parts per row: as many as it takes to give every SM `want` blocks, at most 8,
 // and none shorter than one round of the loop.
-int parts_for(int64_t T, int64_t V, int elem, int sms) {
-  const int64_t round = (int64_t)kThreads * kUnroll * (16 / elem);
+int parts_for(int64_t T, int64_t V, int elem, int sms, int threads) {
+  const int64_t round = (int64_t)threads * kUnroll * (16 / elem);
   int parts = 1;
   while (parts < kMaxParts && T * parts < (int64_t)sms * 4 && V > round * parts) parts *= 2;
   return parts;
 }
 
 template <typename K, typename A>
-cudaError_t launch_rows(K kernel, const A& a, cudaStream_t st) {
+cudaError_t launch_rows(K kernel, const A& a, cudaStream_t st, int threads = kThreads) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(a.T * a.parts));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3((unsigned)threads);
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
@@ -778,6 +936,12 @@ cudaError_t launch_rows(K kernel, const A& a, cudaStream_t st) {
 
 int elem_size(int dtype) {
   return dtype == STS_DTYPE_F32 ? 4 : dtype == STS_DTYPE_BF16 || dtype == STS_DTYPE_F16 ? 2 : 0;
+}
+
+template <typename T>
+cudaError_t launch_forward(const FwdArgs& a, int threads, cudaStream_t st) {
+  return threads == 128 ? launch_rows(forward_kernel<T, 128>, a, st, 128)
+                        : launch_rows(forward_kernel<T, 256>, a, st, 256);
 }
 
 constexpr int64_t kMost = (int64_t(1) << 31) - 1;
@@ -820,7 +984,8 @@ extern "C" sts_status sts_token_logprobs(const sts_token_rows* rows, float* logp
   a.ld = rows->ld;
   a.T = rows->T;
   a.V = (int)rows->V;
-  a.parts = parts_for(rows->T, rows->V, elem_size(rows->dtype), sms);
+  const int threads = rows->V <= kShortRow ? 128 : 256;
+  a.parts = parts_for(rows->T, rows->V, elem_size(rows->dtype), sms, threads);
   a.stretch = (int)(((rows->V + a.parts - 1) / a.parts + 63) / 64 * 64);
   a.tokens = rows->tokens;
   a.tokens_ld = rows->tokens_ld;
@@ -837,9 +1002,9 @@ extern "C" sts_status sts_token_logprobs(const sts_token_rows* rows, float* logp
   a.top_logprob = stats->top_logprob;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   const LaunchMark mark = launch_begin(STS_KERNEL_TOKEN_LOGPROBS, st);
-  const cudaError_t e = rows->dtype == STS_DTYPE_F32    ? launch_rows(forward_kernel<float>, a, st)
-                        : rows->dtype == STS_DTYPE_BF16 ? launch_rows(forward_kernel<__nv_bfloat16>, a, st)
-                                                        : launch_rows(forward_kernel<__half>, a, st);
+  const cudaError_t e = rows->dtype == STS_DTYPE_F32    ? launch_forward<float>(a, threads, st)
+                        : rows->dtype == STS_DTYPE_BF16 ? launch_forward<__nv_bfloat16>(a, threads, st)
+                                                        : launch_forward<__half>(a, threads, st);
   launch_end(mark, st);
   return e == cudaSuccess ? STS_OK : STS_ERR_CUDA;
 }
@@ -892,7 +1057,7 @@ extern "C" sts_status sts_token_logprobs_backward(const sts_token_rows* rows,
   a.ld = rows->ld;
   a.T = rows->T;
   a.V = (int)rows->V;
-  a.parts = parts_for(rows->T, rows->V, es, sms);
+  a.parts = parts_for(rows->T, rows->V, es, sms, kThreads);
   a.stretch = (int)(((rows->V + a.parts - 1) / a.parts + 63) / 64 * 64);
   a.tokens = rows->tokens;
   a.tokens_ld = rows->tokens_ld;

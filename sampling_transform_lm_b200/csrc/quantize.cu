@@ -14,11 +14,13 @@
 // enter the scale, so they cost their neighbours no precision, and stay
 // visible as NaN in every product that they take part in.
 //
-// Nothing is used twice: the kernels are bound by HBM. Each block is read once
-// into registers (8 elements a load), its maximum is taken there, and the codes
-// leave 8 bytes a thread:
-//   rows1    x's K is contiguous, blocks of 1 x 128: 16 lanes hold a block, the
-//            maximum is four shuffles. No shared memory, no barrier.
+// Nothing is used twice: HBM bounds the kernels, as long as they stay under some
+// 8 instructions an element. Each block is read once, 16 bytes a load, and kept
+// as it was read; the maximum is taken on packed pairs, and the codes leave 8
+// bytes a store:
+//   rows1    x's K is contiguous, blocks of 1 x 128: 4 lanes hold a block, 32
+//            elements each, so that the scale's division is paid once in 32. No
+//            shared memory, no barrier.
 //   rows128  x's K is contiguous, blocks of 128 x 128: 256 threads hold a block.
 //   cols     x's rows are contiguous (a transposed view): 256 threads hold 128
 //            x 128 elements; the codes cross shared memory, so that both the
@@ -35,40 +37,166 @@ namespace {
 constexpr int kBlock = 128;
 constexpr int kThreads = 256;
 
-__device__ __forceinline__ float to_f32(float v) { return v; }
-__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
-__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
+constexpr float kLargest = 3.402823466e+38f;
 
-// 8 consecutive elements from p, `live` of them present (the others 0).
-template <typename T, bool kVec>
-__device__ __forceinline__ void load8(const T* p, int live, float (&v)[8]) {
-  if (kVec && live >= 8) {
-    constexpr int kWords = (int)sizeof(T) * 8 / 16;
-    union {
-      uint4 w[kWords];
-      T e[8];
-    } u;
+// 8 consecutive elements, as they were read. Absent ones are 0.
+template <typename T>
+struct Octet {
+  static constexpr int kWords = (int)sizeof(T) / 2;
+  uint4 w[kWords];
+
+  template <bool kVec>
+  __device__ __forceinline__ void load(const T* p, int live) {
+    if (kVec && live >= 8) {
 #pragma unroll
-    for (int i = 0; i < kWords; ++i) u.w[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+      for (int i = 0; i < kWords; ++i) w[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+    } else {
+      union {
+        uint4 q[kWords];
+        T e[8];
+      } u;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = to_f32(u.e[i]);
-  } else {
+      for (int i = 0; i < kWords; ++i) u.q[i] = make_uint4(0, 0, 0, 0);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = i < live ? to_f32(p[i]) : 0.f;
+      for (int i = 0; i < 8; ++i)
+        if (i < live) u.e[i] = p[i];
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) w[i] = u.q[i];
+    }
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const;
+  __device__ __forceinline__ float at(int j) const {  // j a constant where it is called
+    float v[8];
+    get(v);
+    return v[j];
+  }
+};
+
+__device__ __forceinline__ void words(const uint4& w, uint32_t (&u)[4]) {
+  u[0] = w.x;
+  u[1] = w.y;
+  u[2] = w.z;
+  u[3] = w.w;
+}
+
+template <>
+__device__ __forceinline__ void Octet<float>::get(float (&v)[8]) const {
+  uint32_t u[4];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    words(w[h], u);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[4 * h + i] = __uint_as_float(u[i]);
+  }
+}
+template <>
+__device__ __forceinline__ void Octet<__nv_bfloat16>::get(float (&v)[8]) const {
+  uint32_t u[4];
+  words(w[0], u);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {  // a bf16 is the upper half of its fp32
+    v[2 * i] = __uint_as_float(u[i] << 16);
+    v[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+  }
+}
+template <>
+__device__ __forceinline__ void Octet<__half>::get(float (&v)[8]) const {
+  uint32_t u[4];
+  words(w[0], u);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u[i]));
+    v[2 * i] = f.x;
+    v[2 * i + 1] = f.y;
   }
 }
 
-constexpr float kLargest = 3.402823466e+38f;
+// Element-wise largest |.| of octets (a NaN is passed over), on packed pairs.
+template <typename T>
+struct Largest;
 
-// The largest finite |v|, 0 without one.
-__device__ __forceinline__ float largest8(const float (&v)[8]) {
-  float m = 0.f;
+template <>
+struct Largest<float> {
+  float m[8];
+  __device__ __forceinline__ Largest() {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[i]));  // a NaN is passed over
-  if (m > kLargest) {  // an infinity among them
+    for (int i = 0; i < 8; ++i) m[i] = 0.f;
+  }
+  __device__ __forceinline__ void add(const Octet<float>& o) {
+    float v[8];
+    o.get(v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m[i] = fmaxf(m[i], fabsf(v[i]));
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = m[i];
+  }
+};
+
+template <typename P>
+struct LargestPairs {
+  P m[4];
+  __device__ __forceinline__ LargestPairs() {
+    const uint32_t zero = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m[i] = *reinterpret_cast<const P*>(&zero);
+  }
+  template <typename T>
+  __device__ __forceinline__ void add(const Octet<T>& o) {
+    uint32_t u[4];
+    words(o.w[0], u);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m[i] = __hmax2(m[i], __habs2(*reinterpret_cast<const P*>(&u[i])));
+  }
+};
+template <>
+struct Largest<__nv_bfloat16> : LargestPairs<__nv_bfloat162> {
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = __bfloat1622float2(m[i]);
+      v[2 * i] = f.x;
+      v[2 * i + 1] = f.y;
+    }
+  }
+};
+template <>
+struct Largest<__half> : LargestPairs<__half2> {
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = __half22float2(m[i]);
+      v[2 * i] = f.x;
+      v[2 * i + 1] = f.y;
+    }
+  }
+};
+
+__device__ __forceinline__ float most(const float (&v)[8]) {
+  return fmaxf(fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])),
+               fmaxf(fmaxf(v[4], v[5]), fmaxf(v[6], v[7])));
+}
+
+// The largest finite |.| of kN octets; `inf` where an infinity is among them
+// (they are then looked through once more without it).
+template <typename T, int kN>
+__device__ __forceinline__ float largest_of(const Octet<T> (&o)[kN], bool& inf) {
+  Largest<T> l;
+#pragma unroll
+  for (int i = 0; i < kN; ++i) l.add(o[i]);
+  float v[8];
+  l.get(v);
+  float m = most(v);
+  inf = m > kLargest;
+  if (inf) {
     m = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[i]) <= kLargest ? fabsf(v[i]) : 0.f);
+    for (int i = 0; i < kN; ++i) {
+      o[i].get(v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) m = fmaxf(m, fabsf(v[j]) <= kLargest ? fabsf(v[j]) : 0.f);
+    }
   }
   return m;
 }
@@ -93,8 +221,9 @@ __device__ __forceinline__ uint32_t code2(float a, float b) {
                                             kE5 ? __NV_E5M2 : __NV_E4M3);
 }
 
+// Codes of 8 entries; `inf`: infinities may be among them.
 template <bool kE5>
-__device__ __forceinline__ uint2 code8(const float (&v)[8], const Scale& sc) {
+__device__ __forceinline__ uint2 code8(const float (&v)[8], const Scale& sc, bool inf) {
   float y[8];
   if (sc.s >= 1.17549435e-38f) {
 #pragma unroll
@@ -103,15 +232,10 @@ __device__ __forceinline__ uint2 code8(const float (&v)[8], const Scale& sc) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) y[i] = __fdiv_rn(v[i], sc.s);
   }
-  // the conversion limits what is too large, infinities included: NaN for those
-  // (inf times a reciprocal is inf; a finite entry gives at most about top)
-  float m = 0.f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(y[i]));
-  if (m > kLargest) {
+  if (inf) {  // the conversion would limit them to +-top
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (fabsf(y[i]) > kLargest) y[i] = __int_as_float(0x7fc00000);
+      if (fabsf(v[i]) > kLargest) y[i] = __int_as_float(0x7fc00000);
   }
   uint2 w;
   w.x = code2<kE5>(y[0], y[1]) | (code2<kE5>(y[2], y[3]) << 16);
@@ -137,57 +261,40 @@ struct QuantArgs {
   float* scale;
   int64_t scale_ld;
   int64_t row_blocks, k_blocks;
+  int width;   // rows1: blocks along K per thread block
   bool q_vec;  // q rows start on 8-byte boundaries
 };
 
-// 1 x 128 blocks along contiguous K: 16 lanes a block, kUnroll blocks in flight
-// for each group of lanes.
+// 1 x 128 blocks along contiguous K: 4 lanes a block, 64 blocks a thread block
+// (`width` of them, a power of two, along K and 64 / width rows). Lane i of the
+// four holds the 16-byte pieces i, i + 4, ..
 template <typename T, bool kE5, bool kVec>
 __global__ void __launch_bounds__(kThreads) rows1_kernel(const QuantArgs a) {
-  constexpr int kUnroll = sizeof(T) == 2 ? 4 : 2;
-  const int sub = threadIdx.x & 15;
-  const int64_t total = a.R * a.k_blocks;
-  const int64_t groups = (int64_t)gridDim.x * (kThreads / 16);
-  for (int64_t first = (int64_t)blockIdx.x * (kThreads / 16) + (threadIdx.x >> 4); first < total;
-       first += groups * kUnroll) {
-    float v[kUnroll][8];
-    int64_t row[kUnroll];
-    int64_t kb[kUnroll];
-    int live[kUnroll];
+  const int sub = threadIdx.x & 3, at = threadIdx.x >> 2;
+  const int64_t r = (int64_t)blockIdx.x * (64 / a.width) + at / a.width;
+  for (int64_t kb = (int64_t)blockIdx.y * a.width + at % a.width;; kb += (int64_t)gridDim.y * a.width) {
+    // the four lanes of a block agree; whole warps leave together
+    const bool mine = r < a.R && kb < a.k_blocks;
+    if (__ballot_sync(0xFFFFFFFFu, mine) == 0) break;
+    const int64_t k = kb * kBlock + sub * 8;
+    const T* x = static_cast<const T*>(a.x) + r * a.ld + k;
+    const int left = mine ? (int)min(a.K - k, (int64_t)kBlock) : 0;
+    Octet<T> o[4];
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int64_t b = first + u * groups;
-      live[u] = 0;
-      if (b < total) {
-        if (total <= 0xFFFFFFFFll) {  // a 32-bit division wherever it will do
-          row[u] = (int64_t)((uint32_t)b / (uint32_t)a.k_blocks);
-        } else {
-          row[u] = b / a.k_blocks;
-        }
-        kb[u] = b - row[u] * a.k_blocks;
-        const int64_t left = a.K - (kb[u] * kBlock + sub * 8);
-        live[u] = left >= 8 ? 8 : (left > 0 ? (int)left : 0);
-        if (live[u] > 0)
-          load8<T, kVec>(static_cast<const T*>(a.x) + row[u] * a.ld + kb[u] * kBlock + sub * 8,
-                         live[u], v[u]);
-      }
-    }
+    for (int i = 0; i < 4; ++i) o[i].template load<kVec>(x + 32 * i, left - 32 * i);
+    bool inf;
+    float m = largest_of(o, inf);
+    m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+    m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+    if (!mine) continue;
+    const Scale s = block_scale<kE5>(m);
+    if (sub == 0) a.scale[r * a.scale_ld + kb] = s.s;
+    uint8_t* q = a.q + r * a.q_ld + k;
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const bool mine = first + u * groups < total;
-      float m = 0.f;
-      if (live[u] > 0) m = largest8(v[u]);
-      // the 16 lanes of a group agree on `first`, but the two groups of a warp
-      // may leave the loop apart: only this group's lanes take part
-      const uint32_t lanes = 0xFFFFu << (threadIdx.x & 16);
-#pragma unroll
-      for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(lanes, m, o));
-      if (!mine) continue;
-      const Scale s = block_scale<kE5>(m);
-      if (sub == 0) a.scale[row[u] * a.scale_ld + kb[u]] = s.s;
-      if (live[u] > 0)
-        store8(a.q + row[u] * a.q_ld + kb[u] * kBlock + sub * 8, code8<kE5>(v[u], s), live[u],
-               a.q_vec);
+    for (int i = 0; i < 4; ++i) {
+      float v[8];
+      o[i].get(v);
+      store8(q + 32 * i, code8<kE5>(v, s, inf), left - 32 * i, a.q_vec);
     }
   }
 }
@@ -206,7 +313,7 @@ __device__ __forceinline__ float block_max(float m, float* warp_max) {
 // 128 x 128 blocks along contiguous K: one block per thread block, thread t
 // holds 8 columns of the rows t / 16 + 16 i.
 template <typename T, bool kE5, bool kVec>
-__global__ void __launch_bounds__(kThreads) rows128_kernel(const QuantArgs a) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2) rows128_kernel(const QuantArgs a) {
   __shared__ float warp_max[kThreads / 32];
   const int64_t rb = (int64_t)blockIdx.x / a.k_blocks;
   const int64_t kb = (int64_t)blockIdx.x - rb * a.k_blocks;
@@ -214,21 +321,22 @@ __global__ void __launch_bounds__(kThreads) rows128_kernel(const QuantArgs a) {
   const int64_t left = a.K - k;
   const int live = left >= 8 ? 8 : (left > 0 ? (int)left : 0);
   const int64_t r0 = rb * kBlock + (threadIdx.x >> 4);
-  float v[8][8];
-  float m = 0.f;
+  Octet<T> o[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int64_t r = r0 + 16 * i;
-    load8<T, kVec>(static_cast<const T*>(a.x) + r * a.ld + k, r < a.R ? live : 0, v[i]);
+    o[i].template load<kVec>(static_cast<const T*>(a.x) + r * a.ld + k, r < a.R ? live : 0);
   }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) m = fmaxf(m, largest8(v[i]));
+  bool inf;
+  const float m = largest_of(o, inf);
   const Scale s = block_scale<kE5>(block_max(m, warp_max));
   if (threadIdx.x == 0) a.scale[rb * a.scale_ld + kb] = s.s;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int64_t r = r0 + 16 * i;
-    if (r < a.R) store8(a.q + r * a.q_ld + k, code8<kE5>(v[i], s), live, a.q_vec);
+    float v[8];
+    o[i].get(v);
+    if (r < a.R) store8(a.q + r * a.q_ld + k, code8<kE5>(v, s, inf), live, a.q_vec);
   }
 }
 
@@ -238,7 +346,7 @@ __global__ void __launch_bounds__(kThreads) rows128_kernel(const QuantArgs a) {
 // group index exclusive-ored with row / 8 so that neither side meets a bank
 // conflict.
 template <typename T, bool kE5, bool kVec, bool kSquare>
-__global__ void __launch_bounds__(kThreads) cols_kernel(const QuantArgs a) {
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 3 : 2) cols_kernel(const QuantArgs a) {
   __shared__ float warp_max[kThreads / 32];
   __shared__ float row_max[16][kBlock + 1];
   __shared__ uint2 codes[kBlock][16];
@@ -249,31 +357,42 @@ __global__ void __launch_bounds__(kThreads) cols_kernel(const QuantArgs a) {
   const int64_t k = kb * kBlock + kg * 8;
   const int64_t left = a.R - r;
   const int live = left >= 8 ? 8 : (left > 0 ? (int)left : 0);
-  float v[8][8];  // [k][r]
+  Octet<T> o[8];  // [k]: 8 rows each
 #pragma unroll
   for (int i = 0; i < 8; ++i)
-    load8<T, kVec>(static_cast<const T*>(a.x) + (k + i) * a.ld + r, k + i < a.K ? live : 0, v[i]);
+    o[i].template load<kVec>(static_cast<const T*>(a.x) + (k + i) * a.ld + r, k + i < a.K ? live : 0);
   Scale s[kSquare ? 1 : 8];
+  bool inf;
   if constexpr (kSquare) {
-    float m = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) m = fmaxf(m, largest8(v[i]));
+    const float m = largest_of(o, inf);
     s[0] = block_scale<kE5>(block_max(m, warp_max));
     if (threadIdx.x == 0) a.scale[rb * a.scale_ld + kb] = s[0].s;
   } else {
+    Largest<T> l;  // of each of the 8 rows
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      float w[8];
+    for (int i = 0; i < 8; ++i) l.add(o[i]);
+    float m[8];
+    l.get(m);
+    inf = most(m) > kLargest;
+    if (inf) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) w[i] = v[i][j];
-      row_max[kg][oct * 8 + j] = largest8(w);
+      for (int j = 0; j < 8; ++j) m[j] = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        float v[8];
+        o[i].get(v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) m[j] = fmaxf(m[j], fabsf(v[j]) <= kLargest ? fabsf(v[j]) : 0.f);
+      }
     }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) row_max[kg][oct * 8 + j] = m[j];
     __syncthreads();
     if (threadIdx.x < kBlock) {
-      float m = 0.f;
+      float x = 0.f;
 #pragma unroll
-      for (int g = 0; g < 16; ++g) m = fmaxf(m, row_max[g][threadIdx.x]);
-      const Scale sc = block_scale<kE5>(m);
+      for (int g = 0; g < 16; ++g) x = fmaxf(x, row_max[g][threadIdx.x]);
+      const Scale sc = block_scale<kE5>(x);
       row_max[0][threadIdx.x] = sc.s;
       row_max[1][threadIdx.x] = sc.inv;
       const int64_t row = rb * kBlock + threadIdx.x;
@@ -290,8 +409,8 @@ __global__ void __launch_bounds__(kThreads) cols_kernel(const QuantArgs a) {
   for (int j = 0; j < 8; ++j) {
     float w[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = v[i][j];
-    codes[oct * 8 + j][kg ^ oct] = code8<kE5>(w, s[kSquare ? 0 : j]);
+    for (int i = 0; i < 8; ++i) w[i] = o[i].at(j);
+    codes[oct * 8 + j][kg ^ oct] = code8<kE5>(w, s[kSquare ? 0 : j], inf);
   }
   __syncthreads();
   const int64_t kk = kb * kBlock + oct * 8;  // now 16 lanes write a row's 128 codes
@@ -306,12 +425,12 @@ __global__ void __launch_bounds__(kThreads) cols_kernel(const QuantArgs a) {
 }
 
 template <typename T, bool kE5, bool kVec>
-cudaError_t launch(const QuantArgs& a, bool transposed, int block_rows, int sms, cudaStream_t st) {
+cudaError_t launch(const QuantArgs& a, bool transposed, int block_rows, cudaStream_t st) {
   if (!transposed && block_rows == 1) {
-    constexpr int64_t per = kThreads / 16;
-    const int64_t want = (a.R * a.k_blocks + per - 1) / per;
-    const int64_t most = (int64_t)sms * 16;  // 2,048 threads an SM, two blocks deep
-    rows1_kernel<T, kE5, kVec><<<(int)(want < most ? want : most), kThreads, 0, st>>>(a);
+    const int64_t rows = 64 / a.width;
+    const int64_t along = (a.k_blocks + a.width - 1) / a.width;
+    const dim3 grid((unsigned)((a.R + rows - 1) / rows), (unsigned)(along < 65535 ? along : 65535));
+    rows1_kernel<T, kE5, kVec><<<grid, kThreads, 0, st>>>(a);
     return cudaGetLastError();
   }
   const unsigned grid = (unsigned)(a.row_blocks * a.k_blocks);
@@ -325,16 +444,16 @@ cudaError_t launch(const QuantArgs& a, bool transposed, int block_rows, int sms,
 }
 
 template <typename T>
-cudaError_t launch_t(const QuantArgs& a, bool e5, bool transposed, int block_rows, int sms,
+cudaError_t launch_t(const QuantArgs& a, bool e5, bool transposed, int block_rows,
                      cudaStream_t st) {
   // 16-byte loads need 16-byte rows; any other layout is read element by element
   const bool vec = (reinterpret_cast<uintptr_t>(a.x) & 15u) == 0 &&
                    (a.ld * (int64_t)sizeof(T)) % 16 == 0;
   if (vec)
-    return e5 ? launch<T, true, true>(a, transposed, block_rows, sms, st)
-              : launch<T, false, true>(a, transposed, block_rows, sms, st);
-  return e5 ? launch<T, true, false>(a, transposed, block_rows, sms, st)
-            : launch<T, false, false>(a, transposed, block_rows, sms, st);
+    return e5 ? launch<T, true, true>(a, transposed, block_rows, st)
+              : launch<T, false, true>(a, transposed, block_rows, st);
+  return e5 ? launch<T, true, false>(a, transposed, block_rows, st)
+            : launch<T, false, false>(a, transposed, block_rows, st);
 }
 
 }  // namespace
@@ -372,6 +491,10 @@ extern "C" sts_status sts_block_quantize(int64_t R, int64_t K, const void* x, in
   a.scale_ld = scale_ld;
   a.row_blocks = (R + kBlock - 1) / kBlock;
   a.k_blocks = k_blocks;
+  // as many blocks along K as leave at most an eighth of them without work
+  a.width = 64;
+  while (a.width > 1 && ((k_blocks + a.width - 1) / a.width * a.width - k_blocks) * 8 > k_blocks)
+    a.width /= 2;
   a.q_vec = (reinterpret_cast<uintptr_t>(q) & 7u) == 0 && q_ld % 8 == 0;
   if (a.row_blocks * k_blocks > kMost) return STS_ERR_SHAPE;
   int sms = 0;
@@ -381,9 +504,9 @@ extern "C" sts_status sts_block_quantize(int64_t R, int64_t K, const void* x, in
   const LaunchMark mark = launch_begin(STS_KERNEL_BLOCK_QUANTIZE, st);
   const bool e5 = q_dtype == STS_DTYPE_E5M2;
   const cudaError_t e =
-      x_dtype == STS_DTYPE_F32    ? launch_t<float>(a, e5, transposed, block_rows, sms, st)
-      : x_dtype == STS_DTYPE_BF16 ? launch_t<__nv_bfloat16>(a, e5, transposed, block_rows, sms, st)
-                                  : launch_t<__half>(a, e5, transposed, block_rows, sms, st);
+      x_dtype == STS_DTYPE_F32    ? launch_t<float>(a, e5, transposed, block_rows, st)
+      : x_dtype == STS_DTYPE_BF16 ? launch_t<__nv_bfloat16>(a, e5, transposed, block_rows, st)
+                                  : launch_t<__half>(a, e5, transposed, block_rows, st);
   launch_end(mark, st);
   return e == cudaSuccess ? STS_OK : STS_ERR_CUDA;
 }
