@@ -18,9 +18,10 @@
 // Any base gives the same quotients, so b is c times the maximum of the first
 // chunk of 2,048 to 8,192 elements and moves, a thread at a time, only when an
 // element exceeds it by more than a factor of 2 (a larger x would carry a larger
-// rounding into the terms that matter). An element costs a clamp, two FMAs (c
-// in two parts: the rounding of one would be a common factor of all x), an
-// exponential and two sums. The clamp keeps x at -200 or above (2^-200 is 0 in
+// rounding into the terms that matter). An element costs a clamp, an FMA, an
+// exponential and two sums; fp32 logits a second FMA, for what c's rounding
+// leaves (16-bit logits are themselves rounded by 2^-9 or 2^-11; there c's 2^-24
+// is a temperature half a step off, put right in log_sum by its derivative). The clamp keeps x at -200 or above (2^-200 is 0 in
 // fp32), so that masked logits put no 0 * inf into S'_1. Each thread's sums
 // (fp32, two of each) are joined in float64. Rows whose largest c z_i leaves
 // fp32's exact range, 2^20 (nothing but masks of the type's lowest value, say),
@@ -34,6 +35,10 @@
 // Keys that outgrow the buffer (ascending rows, rows of equal logits) are
 // dropped and the row's share is searched again digit by digit.
 //
+// The logits come by bulk copies into two buffers of shared memory a block, so
+// that the next chunk is on its way while one is summed, without a register
+// spent on it; the last warp to have read a buffer orders its next chunk.
+//
 // A row is a thread block's, or, where there are too few rows to fill the
 // GPU, that of a cluster of 2, 4 or 8 blocks, each with a stretch of the
 // vocabulary; the first block joins their results over distributed shared
@@ -45,7 +50,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
-#include "sts_internal.h"
+#include "sts_device.cuh"
 
 namespace sts {
 namespace {
@@ -54,6 +59,7 @@ namespace cg = cooperative_groups;
 
 constexpr int kThreads = 256;     // of the gradient, and of the forward for long rows
 constexpr int kUnroll = 4;       // 16-byte loads in flight per thread
+constexpr int kBuffers = 2;      // of one chunk each: threads x kUnroll x 16 bytes
 constexpr int kMaxTop = 64;      // alternatives per row
 constexpr int kMaxGiven = 512;   // given tokens per row
 constexpr int kMaxParts = 8;     // portable cluster size
@@ -93,7 +99,6 @@ template <typename T>
 struct Vec {
   static constexpr int kN = 16 / (int)sizeof(T);
   uint4 w;
-  __device__ __forceinline__ void load(const T* p) { w = __ldg(reinterpret_cast<const uint4*>(p)); }
   __device__ __forceinline__ void none() {  // all -inf
     constexpr uint32_t k = std::is_same<T, float>::value           ? 0xFF800000u
                            : std::is_same<T, __nv_bfloat16>::value ? 0xFF80FF80u
@@ -101,7 +106,6 @@ struct Vec {
     w = make_uint4(k, k, k, k);
   }
   __device__ __forceinline__ void f32(float (&v)[kN]) const;
-  __device__ __forceinline__ float largest() const;  // NaN where one is NaN
   __device__ __forceinline__ float at(int k) const {  // one element, chosen at run time
     constexpr int kPer = 4 / (int)sizeof(T);
     const int i = k / kPer;
@@ -120,11 +124,6 @@ __device__ __forceinline__ void Vec<float>::f32(float (&v)[4]) const {
   v[3] = __uint_as_float(w.w);
 }
 template <>
-__device__ __forceinline__ float Vec<float>::largest() const {
-  return max_nan(max_nan(__uint_as_float(w.x), __uint_as_float(w.y)),
-                 max_nan(__uint_as_float(w.z), __uint_as_float(w.w)));
-}
-template <>
 __device__ __forceinline__ void Vec<__nv_bfloat16>::f32(float (&v)[8]) const {
   const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
@@ -132,12 +131,6 @@ __device__ __forceinline__ void Vec<__nv_bfloat16>::f32(float (&v)[8]) const {
     v[2 * i] = __uint_as_float(u[i] << 16);
     v[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
   }
-}
-template <>
-__device__ __forceinline__ float Vec<__nv_bfloat16>::largest() const {
-  const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&w);
-  const float2 f = __bfloat1622float2(__hmax2_nan(__hmax2_nan(h[0], h[1]), __hmax2_nan(h[2], h[3])));
-  return max_nan(f.x, f.y);
 }
 template <>
 __device__ __forceinline__ void Vec<__half>::f32(float (&v)[8]) const {
@@ -149,11 +142,37 @@ __device__ __forceinline__ void Vec<__half>::f32(float (&v)[8]) const {
     v[2 * i + 1] = f.y;
   }
 }
-template <>
-__device__ __forceinline__ float Vec<__half>::largest() const {
-  const __half2* h = reinterpret_cast<const __half2*>(&w);
-  const float2 f = __half22float2(__hmax2_nan(__hmax2_nan(h[0], h[1]), __hmax2_nan(h[2], h[3])));
-  return max_nan(f.x, f.y);
+// The largest element of kM vectors, NaN where one is NaN.
+template <typename P, int kM>
+__device__ __forceinline__ P largest_pairs(const uint4* w) {
+  P m[4];
+#pragma unroll
+  for (int u = 0; u < kM; ++u) {
+    const P* h = reinterpret_cast<const P*>(w + u);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m[i] = u == 0 ? h[i] : __hmax2_nan(m[i], h[i]);
+  }
+  return __hmax2_nan(__hmax2_nan(m[0], m[1]), __hmax2_nan(m[2], m[3]));
+}
+template <typename T, int kM>
+__device__ __forceinline__ float largest(const Vec<T> (&v)[kM]) {
+  uint4 w[kM];
+#pragma unroll
+  for (int u = 0; u < kM; ++u) w[u] = v[u].w;
+  if constexpr (std::is_same<T, float>::value) {
+    float m = kNegInf;
+#pragma unroll
+    for (int u = 0; u < kM; ++u)
+      m = max_nan(max_nan(m, max_nan(__uint_as_float(w[u].x), __uint_as_float(w[u].y))),
+                  max_nan(__uint_as_float(w[u].z), __uint_as_float(w[u].w)));
+    return m;
+  } else if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+    const float2 f = __bfloat1622float2(largest_pairs<__nv_bfloat162, kM>(w));
+    return max_nan(f.x, f.y);
+  } else {
+    const float2 f = __half22float2(largest_pairs<__half2, kM>(w));
+    return max_nan(f.x, f.y);
+  }
 }
 
 // fp32 bits as an unsigned number of the same order; -0 counts as +0.
@@ -196,6 +215,10 @@ struct Share {  // what one block found in its stretch
 
 template <int kT>
 struct FwdSmem {
+  uint4 ring[kBuffers][kT * kUnroll];
+  uint64_t full[kBuffers];
+  uint32_t read[kBuffers];  // warps that have read the buffer
+  int abort;
   uint64_t keys[kKeyCap];
   uint64_t top[kMaxTop];
   uint64_t lists[kMaxParts][kMaxTop];
@@ -277,7 +300,7 @@ __device__ __forceinline__ void rebase(Sums& s, float to, Factor& c) {
   c.far = far;
 }
 
-template <bool kFarForm>
+template <bool kFarForm, bool kTwo>
 __device__ __forceinline__ void add(Sums& s, int h, float z, const Factor& c) {
   float x;
   if (kFarForm) {
@@ -286,7 +309,8 @@ __device__ __forceinline__ void add(Sums& s, int h, float z, const Factor& c) {
     x = fmaxf(fmaf(d, c.lo, d * c.hi), -200.f);
   } else {
     const float y = fmaxf(z, s.least);
-    x = fmaf(y, c.lo, fmaf(y, c.hi, -s.b));
+    x = fmaf(y, c.hi, -s.b);
+    if (kTwo) x = fmaf(y, c.lo, x);
   }
   const float e = ex2(x);
   s.s0[h] += e;
@@ -299,13 +323,10 @@ __device__ __forceinline__ void keep(FwdSmem<kT>& sm, float z, uint32_t id) {
   if (at < (uint32_t)kKeyCap) sm.keys[at] = token_key(z, id);
 }
 
-// An element on its own (a head, a tail, or one of a vector above the bound):
-// keep it where it is above `cut`, and move the base where it must.
 template <int kT>
-__device__ __forceinline__ void consider(FwdSmem<kT>& sm, Sums& s, float z, Factor& c,
-                                         uint32_t id, float cut, bool or_equal) {
+__device__ __forceinline__ void keep_above(FwdSmem<kT>& sm, float z, uint32_t id, float cut,
+                                           bool or_equal) {
   if (z > cut || (or_equal && z == cut && z > kNegInf)) keep(sm, z, id);
-  if ((z - s.base) * c.hi > 1.f && z < INFINITY) rebase(s, z, c);
 }
 
 // The n largest of the stretch, digit by digit, for rows whose keys did not
@@ -381,15 +402,13 @@ __device__ __noinline__ int search_again(FwdSmem<kT>& sm, const T* z, int len, u
   return (int)min(sm.count, (uint32_t)kKeyCap);
 }
 
-// The first bound, from one chunk (vm: the maxima of this thread's vectors):
+// The first bound, from one chunk (m: the maximum of this thread's vectors):
 // sm.cut is the n-th largest of `groups` group maxima, and sm.chunk_max the
 // largest; -inf where fewer than n groups hold anything. NaN counts as nothing.
 template <int kT>
-__device__ __forceinline__ void first_bound(FwdSmem<kT>& sm, const float (&vm)[kUnroll], int groups,
-                                            int n) {
+__device__ __forceinline__ void first_bound(FwdSmem<kT>& sm, float m, int groups, int n) {
   const int tid = threadIdx.x;
   const int per_group = kT / groups;
-  float m = fmaxf(fmaxf(vm[0], vm[1]), fmaxf(vm[2], vm[3]));
   for (int o = 1; o < per_group; o *= 2) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
   if ((tid & (per_group - 1)) == 0) sm.group_max[tid / per_group] = m;
   if (tid == 0) sm.cut = kNegInf;
@@ -413,8 +432,11 @@ __device__ __forceinline__ void first_bound(FwdSmem<kT>& sm, const float (&vm)[k
 
 template <typename T, int kT>
 __global__ void __launch_bounds__(kT, 1024 / kT) forward_kernel(const FwdArgs a) {
-  __shared__ FwdSmem<kT> sm;
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  FwdSmem<kT>& sm = *reinterpret_cast<FwdSmem<kT>*>(smem_raw);
   constexpr int kN = Vec<T>::kN;
+  constexpr int kChunk = kT * kUnroll;  // vectors
+  constexpr bool kTwo = sizeof(T) == 4;  // c in two parts
   const int parts = a.parts;
   const int64_t row = (int64_t)blockIdx.x / parts;
   const int part = (int)((int64_t)blockIdx.x - row * parts);
@@ -438,7 +460,26 @@ __global__ void __launch_bounds__(kT, 1024 / kT) forward_kernel(const FwdArgs a)
   const int tail0 = head + body * kN;
   const T* zb = z + head;
 
-  if (tid == 0) sm.count = 0;
+  // chunk number i of the stretch into its buffer
+  auto order = [&](int i) {
+    const int i0 = i * kChunk, n16 = min(kChunk, body - i0);
+    const uint32_t bar = smem_u32(&sm.full[i % kBuffers]);
+    mbar_arrive_expect_tx(bar, (uint32_t)n16 * 16u);
+    bulk_load(smem_u32(sm.ring[i % kBuffers]), zb + (int64_t)i0 * kN, (uint32_t)n16 * 16u, bar);
+  };
+  const int chunks = (body + kChunk - 1) / kChunk;
+  if (tid == 0) {
+    sm.count = 0;
+    sm.abort = 0;
+    for (int b = 0; b < kBuffers; ++b) {
+      mbar_init(smem_u32(&sm.full[b]), 1);
+      sm.read[b] = 0;
+    }
+    fence_barrier_init();
+    fence_proxy_async_smem();
+    for (int i = 0; i < min(kBuffers, chunks); ++i) order(i);
+  }
+  __syncthreads();
 
   Sums s{{0.f, 0.f}, {0.f, 0.f}, kLowest, 0.f, kLowest};
   float cut = kNegInf;   // nothing at or below it can be an alternative any more
@@ -449,27 +490,32 @@ __global__ void __launch_bounds__(kT, 1024 / kT) forward_kernel(const FwdArgs a)
   bool bound = false;  // a finite bound has been found (the same in every thread)
   // the keys are about n by the first chunk, n more for each doubling of the row
   int next_tighten = n > 16 ? 2 : 4;
-  for (int it = 0, i0 = 0; i0 < body || it == 0; ++it, i0 += kT * kUnroll) {
+  bool late = false;  // a copy that never came
+  for (int it = 0; it < max(chunks, 1); ++it) {
+    const int i0 = it * kChunk, buf = it % kBuffers;
     Vec<T> v[kUnroll];
-    float vm[kUnroll];
-    if (i0 + kT * kUnroll <= body) {
+    if (it < chunks) {
+      late |= !mbar_wait_soon(smem_u32(&sm.full[buf]), (uint32_t)(it / kBuffers) & 1u, &sm.abort, nullptr);
+      if (i0 + kChunk <= body) {
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u) v[u].load(zb + (int64_t)(i0 + u * kT + tid) * kN);
-    } else {
+        for (int u = 0; u < kUnroll; ++u) v[u].w = sm.ring[buf][u * kT + tid];
+      } else {
 #pragma unroll
-      for (int u = 0; u < kUnroll; ++u) {
-        const int i = i0 + u * kT + tid;
-        if (i < body)
-          v[u].load(zb + (int64_t)i * kN);
-        else
-          v[u].none();
+        for (int u = 0; u < kUnroll; ++u) {
+          if (i0 + u * kT + tid < body)
+            v[u].w = sm.ring[buf][u * kT + tid];
+          else
+            v[u].none();
+        }
       }
-    }
+    } else {  // a stretch without a whole vector
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) vm[u] = v[u].largest();
+      for (int u = 0; u < kUnroll; ++u) v[u].none();
+    }
+    const float vmax = largest(v);  // NaN where one is
     bool equal = false;  // whether ties with the bound still count
     if (!bound) {
-      first_bound(sm, vm, groups, n);
+      first_bound(sm, vmax, groups, n);
       if (sm.cut > kNegInf) {
         bound = true;
         equal = true;  // the n elements of the bound are of this very chunk
@@ -493,43 +539,46 @@ __global__ void __launch_bounds__(kT, 1024 / kT) forward_kernel(const FwdArgs a)
       }
       __syncthreads();
     }
-    // vectors with something above the bound, a NaN, or before any bound: looked
-    // at element by element, before their sums, in one rolled loop (rare: about
-    // n elements for each doubling of the row)
-    uint32_t look = 0;
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u)
-      look |= (equal ? !(vm[u] < cut) : !(vm[u] <= cut) || (!bound && vm[u] > kNegInf)) ? 1u << u : 0u;
-    while (look != 0u) {
-      const int u = __ffs((int)look) - 1;
-      look &= look - 1u;
-      Vec<T> x = v[0];
-#pragma unroll
-      for (int i = 1; i < kUnroll; ++i)
-        if (u == i) x = v[i];
-      const uint32_t id = (uint32_t)(v0 + head + (i0 + u * kT + tid) * kN);
-      float f[kN];
-      x.f32(f);
-      uint32_t which = 0;  // its elements above the bound, and NaN
-#pragma unroll
-      for (int k = 0; k < kN; ++k)
-        which |= (equal ? !(f[k] < cut) : !(f[k] <= cut)) ? 1u << k : 0u;
-      while (which != 0u) {
-        const int k = __ffs((int)which) - 1;
-        which &= which - 1u;
-        const float y = x.at(k);
-        seen = max_nan(seen, y);
-        consider(sm, s, y, c, id + (uint32_t)k, cut, equal);
+    // Something above the bound (or at it while ties count), a NaN, or no bound
+    // yet: the warp looks at the thread's elements together, a lane each, in the
+    // buffer (rare: about n elements for each doubling of the row). The thread
+    // moves its base first.
+    const bool look = !(vmax < cut) && (equal || !bound || !(vmax <= cut));
+    uint32_t lookers = __ballot_sync(0xFFFFFFFFu, look);
+    if (lookers != 0u) {
+      if (look) {
+        seen = max_nan(seen, vmax);
+        if ((vmax - s.base) * c.hi > 1.f && vmax < INFINITY) rebase(s, vmax, c);
+      }
+      const int lane = tid & 31;
+      do {
+        const int owner = (tid & ~31) + __ffs((int)lookers) - 1;
+        lookers &= lookers - 1u;
+        const int i = lane / kN * kT + owner;  // of the chunk's vectors
+        if (lane < kUnroll * kN && i0 + i < body) {
+          const float f = to_f32(reinterpret_cast<const T*>(&sm.ring[buf][i])[lane % kN]);
+          keep_above(sm, f, (uint32_t)(v0 + head + (i0 + i) * kN + lane % kN), cut, equal);
+        }
+      } while (lookers != 0u);
+      __syncwarp();
+    }
+    if ((tid & 31) == 0 && it + kBuffers < chunks) {
+      __threadfence_block();
+      if (atomicAdd(&sm.read[buf], 1u) == (uint32_t)(kT / 32 - 1)) {
+        sm.read[buf] = 0;
+        __threadfence_block();
+        fence_proxy_async_smem();
+        order(it + kBuffers);
       }
     }
-    __syncwarp();  // or the lanes that looked would run the rest of the row on their own
+    __syncwarp();
     if (!c.far) {
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
         float f[kN];
         v[u].f32(f);
 #pragma unroll
-        for (int k = 0; k < kN; ++k) add<false>(s, k & 1, f[k], c);
+        for (int k = 0; k < kN; ++k) add<false, kTwo>(s, k & 1, f[k], c);
       }
     } else {
       for (int u = 0; u < kUnroll; ++u) {
@@ -539,21 +588,25 @@ __global__ void __launch_bounds__(kT, 1024 / kT) forward_kernel(const FwdArgs a)
 #pragma unroll
           for (int i = 1; i < kUnroll; ++i)
             if (u == i) x = v[i];
-          add<true>(s, 0, x.at(k), c);
+          add<true, kTwo>(s, 0, x.at(k), c);
         }
       }
     }
   }
+  if (late && (tid & 31) == 0)  // no copy may outlive the block
+    for (int i = max(0, chunks - kBuffers); i < chunks; ++i)
+      mbar_wait_drain(smem_u32(&sm.full[i % kBuffers]), (uint32_t)(i / kBuffers) & 1u);
   // the elements outside the vectors: ids below (head) or above (tail) all others
   for (int i = tid; i < head + (len - tail0); i += kT) {
     const int at = i < head ? i : tail0 + (i - head);
     const float f = to_f32(z[at]);
     seen = max_nan(seen, f);
-    consider(sm, s, f, c, (uint32_t)(v0 + at), cut, true);
+    keep_above(sm, f, (uint32_t)(v0 + at), cut, true);
+    if ((f - s.base) * c.hi > 1.f && f < INFINITY) rebase(s, f, c);
     if (c.far)
-      add<true>(s, 0, f, c);
+      add<true, kTwo>(s, 0, f, c);
     else
-      add<false>(s, 0, f, c);
+      add<false, kTwo>(s, 0, f, c);
   }
 
   // ---- join the block's sums (float64) and find its n largest
@@ -582,7 +635,7 @@ __global__ void __launch_bounds__(kT, 1024 / kT) forward_kernel(const FwdArgs a)
       sm.red0[tid >> 5] = s0;
       sm.red1[tid >> 5] = s1;
     }
-    const int bad = __syncthreads_or(seen != seen || seen == INFINITY);
+    const int bad = __syncthreads_or(late || seen != seen || seen == INFINITY);
     if (tid == 0) {
       s0 = s1 = 0.0;
       for (int w = 0; w < kT / 32; ++w) {
@@ -679,9 +732,13 @@ __global__ void __launch_bounds__(kT, 1024 / kT) forward_kernel(const FwdArgs a)
   const bool empty = reason == 0 && found == 0;
   const float zmax = found > 0 ? key_logit(top[0]) : kNegInf;
   if (tid < 32) {
-    // S = sum 2^(c (z - zmax)); by: what the sums' base is off that
-    const double by = found > 0 ? e - __dmul_rn(cd, (double)zmax) : 0.0;
-    const double ln_total = log(s0 * exp2(by));
+    // S = sum 2^(c (z - zmax)), where c is what the sums were formed with; by:
+    // what their base is off that. What c is off cd moves ln S by d ln S / dc.
+    const bool near = fabsf(zmax * c.hi) < kFar;
+    const double cs = kTwo || !near ? cd : (double)c.hi;
+    const double by = found > 0 ? e - __dmul_rn(cs, (double)zmax) : 0.0;
+    const double mean = s1 / s0 + by;  // of c (z - zmax)
+    const double ln_total = log(s0 * exp2(by)) + kLn2 * (cd / cs - 1.0) * mean;
     const float log_sum = reason ? nan : empty ? kNegInf : (float)ln_total;
     if (tid == 0) {
       sm.log_sum = log_sum;
@@ -690,7 +747,7 @@ __global__ void __launch_bounds__(kT, 1024 / kT) forward_kernel(const FwdArgs a)
       if (a.lse)
         a.lse[row] = reason ? nan : empty ? kNegInf : (float)((double)zmax / (double)tau + ln_total);
       if (a.entropy) {
-        const double h = ln_total - kLn2 * (s1 / s0 + by);
+        const double h = ln_total - kLn2 * (cd / cs) * mean;
         a.entropy[row] = reason ? nan : empty ? 0.f : (float)fmax(h, 0.0);
       }
       if (a.flags)
@@ -917,10 +974,17 @@ int parts_for(int64_t T, int64_t V, int elem, int sms, int threads) {
 }
 
 template <typename K, typename A>
-cudaError_t launch_rows(K kernel, const A& a, cudaStream_t st, int threads = kThreads) {
+cudaError_t launch_rows(K kernel, const A& a, cudaStream_t st, int threads = kThreads,
+                        size_t smem = 0) {
+  if (smem > 48 * 1024) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(a.T * a.parts));
   cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
@@ -940,8 +1004,8 @@ int elem_size(int dtype) {
 
 template <typename T>
 cudaError_t launch_forward(const FwdArgs& a, int threads, cudaStream_t st) {
-  return threads == 128 ? launch_rows(forward_kernel<T, 128>, a, st, 128)
-                        : launch_rows(forward_kernel<T, 256>, a, st, 256);
+  return threads == 128 ? launch_rows(forward_kernel<T, 128>, a, st, 128, sizeof(FwdSmem<128>))
+                        : launch_rows(forward_kernel<T, 256>, a, st, 256, sizeof(FwdSmem<256>));
 }
 
 constexpr int64_t kMost = (int64_t(1) << 31) - 1;
