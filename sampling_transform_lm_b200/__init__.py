@@ -801,45 +801,38 @@ _DTYPE_CODE = {_F32: 0, _BF16: 1, _F16: 2, _E4M3: 3, _E5M2: 4}
 _BLOCK = 128
 
 
-class _Call:
-    """Where one call runs: the tensors' device (made current for the call if it is not) and
-    the given stream, or the device's current one. Outputs are allocated on that stream; with
-    an explicit stream the inputs are recorded on it, so that freeing them early is safe."""
+def _raw_stream(index):
+    return torch.cuda.current_stream(index).cuda_stream
 
-    def __init__(self, stream, *tensors):
-        dev = None
-        for name, t in tensors:
-            if t is None:
-                continue
-            if not t.is_cuda:
-                raise StsError(STS_ERR_SHAPE, f"{name} must be a CUDA tensor")
-            if dev is None:
-                dev = t.device
-            elif t.device != dev:
-                raise StsError(STS_ERR_SHAPE, f"{name} is on {t.device}, expected {dev}")
-        self.device = dev
-        self.contexts = ()
-        if dev.index != torch.cuda.current_device():
-            self.contexts = (torch.cuda.device(dev),)
-        if stream is None:
-            self.stream = torch.cuda.current_stream(dev).cuda_stream
-        else:
-            if stream.device != dev:
-                raise StsError(STS_ERR_SHAPE, f"the stream is on {stream.device}, expected {dev}")
-            self.stream = stream.cuda_stream
-            self.contexts += (torch.cuda.stream(stream),)
-            for _, t in tensors:
-                if t is not None:
-                    t.record_stream(stream)
 
-    def __enter__(self):
-        for c in self.contexts:
-            c.__enter__()
-        return self
+# the same without building a Stream object, where this torch has it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
 
-    def __exit__(self, *exc):
-        for c in reversed(self.contexts):
-            c.__exit__(*exc)
+
+def _place(stream, tensors):
+    """Where a call on these (name, tensor) pairs runs: the tensors' device index, and a context
+    to make the call again in where that is not the current device, or where a stream is given
+    (outputs are then allocated on it, and the inputs recorded, so that freeing them early is
+    safe)."""
+    index = None
+    for name, t in tensors:
+        if t is None:
+            continue
+        i = t.get_device()
+        if i < 0:
+            raise StsError(STS_ERR_SHAPE, f"{name} must be a CUDA tensor")
+        if index is None:
+            index = i
+        elif i != index:
+            raise StsError(STS_ERR_SHAPE, f"{name} is on cuda:{i}, expected cuda:{index}")
+    if stream is None:
+        return index, None if index == torch.cuda.current_device() else torch.cuda.device(index)
+    if stream.device.index != index:
+        raise StsError(STS_ERR_SHAPE, f"the stream is on {stream.device}, expected cuda:{index}")
+    for _, t in tensors:
+        if t is not None:
+            t.record_stream(stream)
+    return index, torch.cuda.stream(stream)
 
 
 def _float_code(t, name, allowed=(_F32, _BF16, _F16)):
@@ -877,21 +870,25 @@ def sts_block_quantize(x, *, block_rows=1, dtype=_E4M3, q=None, scale=None, stre
         sr = max(sr, 1)
     elif R == 1 and sk != 1:
         sr = 1  # one row of strided columns: a transposed view
-    with _Call(stream, ("x", x), ("q", q), ("scale", scale)) as call:
-        blocks = (-(-R // block_rows), -(-K // _BLOCK))
-        if q is None:
-            q = torch.empty((R, -(-K // 16) * 16), dtype=dtype, device=call.device)
-            if q.shape[1] != K:
-                q = q[:, :K]
-        elif q.dtype != dtype or q.shape != x.shape or (K > 1 and q.stride(1) != 1):
-            raise StsError(STS_ERR_SHAPE, f"q must be {dtype} {tuple(x.shape)} with contiguous rows")
-        if scale is None:
-            scale = torch.empty(blocks, dtype=_F32, device=call.device)
-        elif scale.dtype != _F32 or scale.shape != blocks or (blocks[1] > 1 and scale.stride(1) != 1):
-            raise StsError(STS_ERR_SHAPE, f"scale must be fp32 {blocks} with contiguous rows")
-        st = lib.sts_block_quantize(R, K, x.data_ptr(), code, sr, sk, block_rows, _DTYPE_CODE[dtype],
-                                    q.data_ptr(), q.stride(0) if R > 1 else K, scale.data_ptr(),
-                                    scale.stride(0) if blocks[0] > 1 else blocks[1], call.stream)
+    index, elsewhere = _place(stream, (("x", x), ("q", q), ("scale", scale)))
+    if elsewhere is not None:
+        with elsewhere:
+            return sts_block_quantize(x, block_rows=block_rows, dtype=dtype, q=q, scale=scale)
+    blocks = (-(-R // block_rows), -(-K // _BLOCK))
+    if q is None:
+        q = x.new_empty((R, -(-K // 16) * 16), dtype=dtype)
+        if q.shape[1] != K:
+            q = q[:, :K]
+    elif q.dtype != dtype or q.shape != x.shape or (K > 1 and q.stride(1) != 1):
+        raise StsError(STS_ERR_SHAPE, f"q must be {dtype} {tuple(x.shape)} with contiguous rows")
+    if scale is None:
+        scale = x.new_empty(blocks, dtype=_F32)
+    elif scale.dtype != _F32 or scale.shape != blocks or (blocks[1] > 1 and scale.stride(1) != 1):
+        raise StsError(STS_ERR_SHAPE, f"scale must be fp32 {blocks} with contiguous rows")
+    st = lib.sts_block_quantize(R, K, x.data_ptr(), code, sr, sk, block_rows, _DTYPE_CODE[dtype],
+                                q.data_ptr(), q.stride(0) if R > 1 else K, scale.data_ptr(),
+                                scale.stride(0) if blocks[0] > 1 else blocks[1],
+                                _raw_stream(index))
     _check(st, "sts_block_quantize")
     return q, scale
 
@@ -938,24 +935,29 @@ def sts_block_scaled_product(A, a_scale, B, b_scale, *, temperature=None, out=No
             raise StsError(STS_ERR_SHAPE, f"temperature must be contiguous fp32 {(M,)}")
     if accumulate and out is None:
         raise StsError(STS_ERR_NULL, "accumulate needs an out tensor")
-    with _Call(stream, ("A", A), ("a_scale", a_scale), ("B", B), ("b_scale", b_scale),
-               ("temperature", temperature), ("out", out), ("ws", ws)) as call:
-        if out is None:
-            out = torch.empty((M, N), dtype=out_dtype or _F32, device=call.device)
-        elif (out_dtype is not None and out.dtype != out_dtype) or out.shape != (M, N) or (
-                N > 1 and out.stride(1) != 1):
-            raise StsError(STS_ERR_SHAPE, f"out must be {out_dtype or 'fp32 or bf16'} {(M, N)} with "
-                                          "contiguous rows")
-        code = _float_code(out, "out", (_F32, _BF16))
-        if check and ws is None:
-            ws = torch.empty(256, dtype=torch.uint8, device=call.device)
-        st = lib.sts_block_scaled_product(
-            ctypes.byref(a), ctypes.byref(b), K, _at(temperature), out.data_ptr(), code,
-            out.stride(0) if M > 1 else N, 1 if accumulate else 0, _at(ws),
-            0 if ws is None else ws.numel() * ws.element_size(), call.stream)
-        _check(st, "sts_block_scaled_product")
-        if check:
-            sts_get_status(ws, stream, raise_on_error=True)
+    index, elsewhere = _place(stream, (("A", A), ("a_scale", a_scale), ("B", B), ("b_scale", b_scale),
+                                       ("temperature", temperature), ("out", out), ("ws", ws)))
+    if elsewhere is not None:
+        with elsewhere:
+            return sts_block_scaled_product(A, a_scale, B, b_scale, temperature=temperature, out=out,
+                                            out_dtype=out_dtype, accumulate=accumulate, ws=ws,
+                                            check=check)
+    if out is None:
+        out = a_scale.new_empty((M, N), dtype=out_dtype or _F32)
+    elif (out_dtype is not None and out.dtype != out_dtype) or out.shape != (M, N) or (
+            N > 1 and out.stride(1) != 1):
+        raise StsError(STS_ERR_SHAPE, f"out must be {out_dtype or 'fp32 or bf16'} {(M, N)} with "
+                                      "contiguous rows")
+    code = _float_code(out, "out", (_F32, _BF16))
+    if check and ws is None:
+        ws = torch.empty(256, dtype=torch.uint8, device=A.device)
+    st = lib.sts_block_scaled_product(
+        ctypes.byref(a), ctypes.byref(b), K, _at(temperature), out.data_ptr(), code,
+        out.stride(0) if M > 1 else N, 1 if accumulate else 0, _at(ws),
+        0 if ws is None else ws.numel() * ws.element_size(), _raw_stream(index))
+    _check(st, "sts_block_scaled_product")
+    if check:
+        sts_get_status(ws, None, raise_on_error=True)
     return out
 
 
@@ -999,34 +1001,39 @@ def sts_token_logprobs(logits, tokens=None, *, temperature=None, top_n=0, entrop
     T, n = rows.T, rows.top_n
     if n < 0:
         raise StsError(STS_ERR_SHAPE, f"top_n must be 0 or more, got {n}")
-    with _Call(stream, ("logits", logits), ("tokens", tokens), ("temperature", temperature)) as call:
-        dev = call.device
-        stats = torch.empty((4 if entropy else 3, T), dtype=_F32, device=dev).unbind(0)
-        flags = torch.empty(T, dtype=torch.int32, device=dev)
-        saved = {"lse": stats[0], "logit_max": stats[1], "log_sum": stats[2], "flags": flags}
-        if entropy:
-            saved["entropy"] = stats[3]
-        logprob = None
-        if tokens is not None:
-            logprob = torch.empty(tokens.shape, dtype=_F32, device=dev)
-        saved["top_id"] = top_id = torch.empty((T, n), dtype=torch.int64, device=dev)
-        saved["top_logprob"] = top_logprob = torch.empty((T, n), dtype=_F32, device=dev)
-        out = _TokenStats(_at(stats[1]), _at(stats[2]), _at(stats[0]),
-                          _at(stats[3]) if entropy else None, _at(flags), _at(top_id),
-                          _at(top_logprob))
-        st = lib.sts_token_logprobs(ctypes.byref(rows), _at(logprob), ctypes.byref(out), call.stream)
-        _check(st, "sts_token_logprobs")
-        if check:
-            if stream is not None:
-                stream.synchronize()
-            bad = torch.nonzero(flags & ROW_INVALID)
-            if bad.numel():
-                row = int(bad[0])
-                why = int(flags[row])
-                raise StsError(STS_ERR_TEMPERATURE if why & ROW_BAD_TEMPERATURE else
-                               STS_ERR_TARGET if why & ROW_BAD_TARGET else STS_ERR_SHAPE,
-                               f"row {row}" + (" has a NaN or +inf logit" if why & ROW_BAD_LOGIT
-                                               else ""))
+    index, elsewhere = _place(stream, (("logits", logits), ("tokens", tokens),
+                                       ("temperature", temperature)))
+    if elsewhere is not None:
+        with elsewhere:
+            return sts_token_logprobs(logits, tokens, temperature=temperature, top_n=top_n,
+                                      entropy=entropy, check=check)
+    m = rows.m
+    # one allocation for what is fp32
+    sizes = [T, T, T, T * m, T * n] + ([T] if entropy else [])
+    lse, logit_max, log_sum, logprob, top_logprob, *more = logits.new_empty(
+        sum(sizes), dtype=_F32).split_with_sizes(sizes)
+    logprob = None if tokens is None else logprob.view(tokens.shape)
+    top_logprob = top_logprob.view(T, n)
+    flags = logits.new_empty(T, dtype=torch.int32)
+    top_id = logits.new_empty((T, n), dtype=torch.int64)
+    saved = {"lse": lse, "logit_max": logit_max, "log_sum": log_sum, "flags": flags,
+             "top_id": top_id, "top_logprob": top_logprob}
+    if entropy:
+        saved["entropy"] = more[0]
+    out = _TokenStats(logit_max.data_ptr(), log_sum.data_ptr(), lse.data_ptr(),
+                      more[0].data_ptr() if entropy else None, flags.data_ptr(), top_id.data_ptr(),
+                      top_logprob.data_ptr())
+    st = lib.sts_token_logprobs(ctypes.byref(rows), _at(logprob), ctypes.byref(out),
+                                _raw_stream(index))
+    _check(st, "sts_token_logprobs")
+    if check:
+        bad = torch.nonzero(flags & ROW_INVALID)
+        if bad.numel():
+            row = int(bad[0])
+            why = int(flags[row])
+            raise StsError(STS_ERR_TEMPERATURE if why & ROW_BAD_TEMPERATURE else
+                           STS_ERR_TARGET if why & ROW_BAD_TARGET else STS_ERR_SHAPE,
+                           f"row {row}" + (" has a NaN or +inf logit" if why & ROW_BAD_LOGIT else ""))
     return logprob, saved
 
 
@@ -1057,21 +1064,26 @@ def sts_token_logprobs_backward(logits, tokens, saved, grad_logprob=None, *, gra
                                           f"{None if shape is None else tuple(shape)}, got "
                                           f"{t.dtype} {tuple(t.shape)}")
     entropy = None if grad_entropy is None else saved["entropy"]
-    with _Call(stream, ("logits", logits), ("tokens", tokens), ("temperature", temperature),
-               ("logit_max", saved["logit_max"]), ("log_sum", saved["log_sum"]),
-               ("flags", saved["flags"]), ("entropy", entropy), ("top_id", top_id),
-               ("grad_logprob", grad_logprob), ("grad_entropy", grad_entropy), ("grad_top", grad_top),
-               ("out", out)) as call:
-        if out is None:
-            out = torch.empty((T, V), dtype=out_dtype or logits.dtype, device=call.device)
-        elif (out_dtype is not None and out.dtype != out_dtype) or out.shape != (T, V) or (
-                V > 1 and out.stride(1) != 1):
-            raise StsError(STS_ERR_SHAPE, f"out must be {(T, V)} with contiguous rows")
-        code = _float_code(out, "out")
-        stats = _TokenStats(_at(saved["logit_max"]), _at(saved["log_sum"]), None, _at(entropy),
-                            _at(saved["flags"]), _at(top_id), None)
-        st = lib.sts_token_logprobs_backward(
-            ctypes.byref(rows), ctypes.byref(stats), _at(grad_logprob), _at(grad_entropy),
-            _at(grad_top), out.data_ptr(), code, out.stride(0) if T > 1 else V, call.stream)
+    index, elsewhere = _place(stream, (
+        ("logits", logits), ("tokens", tokens), ("temperature", temperature),
+        ("logit_max", saved["logit_max"]), ("log_sum", saved["log_sum"]), ("flags", saved["flags"]),
+        ("entropy", entropy), ("top_id", top_id), ("grad_logprob", grad_logprob),
+        ("grad_entropy", grad_entropy), ("grad_top", grad_top), ("out", out)))
+    if elsewhere is not None:
+        with elsewhere:
+            return sts_token_logprobs_backward(
+                logits, tokens, saved, grad_logprob, grad_entropy=grad_entropy, grad_top=grad_top,
+                temperature=temperature, out=out, out_dtype=out_dtype)
+    if out is None:
+        out = logits.new_empty((T, V), dtype=out_dtype or logits.dtype)
+    elif (out_dtype is not None and out.dtype != out_dtype) or out.shape != (T, V) or (
+            V > 1 and out.stride(1) != 1):
+        raise StsError(STS_ERR_SHAPE, f"out must be {(T, V)} with contiguous rows")
+    code = _float_code(out, "out")
+    stats = _TokenStats(_at(saved["logit_max"]), _at(saved["log_sum"]), None, _at(entropy),
+                        _at(saved["flags"]), _at(top_id), None)
+    st = lib.sts_token_logprobs_backward(
+        ctypes.byref(rows), ctypes.byref(stats), _at(grad_logprob), _at(grad_entropy),
+        _at(grad_top), out.data_ptr(), code, out.stride(0) if T > 1 else V, _raw_stream(index))
     _check(st, "sts_token_logprobs_backward")
     return out
