@@ -59,17 +59,21 @@ constexpr int kStaging = 2048;  // one of a warp's two staging buffers: 32 rows 
 template <int NT, bool kWide, bool kUniform>
 struct Shape {
   static_assert(!kUniform || kWide, "a uniform column scale is the wide form's");
-  static constexpr int kBufs = NT >= 128 ? 2 : 4;
-  static constexpr uint32_t kTmemCols = NT * kBufs;
+  // blocks that change hands together: the accumulators of a group are waited
+  // for, read and given back at once (a handover costs the sums some 300 clocks)
+  static constexpr int kGroupBlocks = kWide ? 1 : NT == 128 ? 2 : 4;
+  static constexpr int kBufs = 2;  // groups of accumulators
+  static constexpr uint32_t kTmemCols = NT * kGroupBlocks * kBufs;
   static constexpr uint32_t kLaneBytes = kLanes * kBlock;
   static constexpr uint32_t kColBytes = NT * kBlock;
   static constexpr uint32_t kStage = kLaneBytes + kColBytes;
   static constexpr int kStages = kWide ? (kUniform ? 4 : 3) : (NT == 128 ? 6 : 8);
   // stages and accumulators repeat together after this many blocks
   static constexpr int kTurn = kStages % kBufs == 0 ? kStages : kStages * kBufs;
-  static constexpr int kSlots = kWide ? 4 : 8;
-  static constexpr int kColScales = kUniform ? 4 : NT;  // floats of a slot beyond the lanes' 128
-  static constexpr uint32_t kSlot = (kLanes + kColScales) * 4;
+  static constexpr int kSlots = 4;  // of a group's scales
+  static constexpr int kColScales = kUniform ? 4 : NT;  // floats of a block's scales beyond the lanes' 128
+  static constexpr uint32_t kBlockScales = kLanes + kColScales;
+  static constexpr uint32_t kSlot = kBlockScales * kGroupBlocks * 4;
   static constexpr uint32_t kStagingBytes = kWide ? kSumWarps * 2 * kStaging : 0;
   static constexpr int kBars = 2 * kStages + 2 * kSlots + 2 * kBufs + 1;
   static constexpr size_t kSmem = (size_t)kStages * kStage + kStagingBytes + kSlots * kSlot + kBars * 8 + 16;
@@ -201,26 +205,20 @@ __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[kN]) {
   }
 }
 
-// Waits for this thread's loads from tensor memory; the registers pass through,
-// so that nothing that uses them moves above the wait.
+// Keeps what uses these registers below this point.
+template <int kN>
+__device__ __forceinline__ void tmem_tie(uint32_t (&r)[kN]) {
+#pragma unroll
+  for (int i = 0; i < kN; i += 8)
+    asm volatile("" : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]),
+                 "+r"(r[i + 5]), "+r"(r[i + 6]), "+r"(r[i + 7]));
+}
+
+// Waits for this thread's loads from tensor memory.
 template <int kN>
 __device__ __forceinline__ void tmem_wait(uint32_t (&r)[kN]) {
-  if constexpr (kN == 32) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-    for (int i = 0; i < 32; i += 8)
-      asm volatile("" : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]),
-                   "+r"(r[i + 5]), "+r"(r[i + 6]), "+r"(r[i + 7]));
-  } else if constexpr (kN == 8) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
-                   "+r"(r[6]), "+r"(r[7])::"memory");
-  } else {
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
-                   "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
-                   "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
-  }
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+  tmem_tie<kN>(r);
 }
 
 // Two fp32 in one register pair; one instruction for both, rounded each.
@@ -250,17 +248,20 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   return d;
 }
 
-// Whether the phase has completed, without waiting.
-__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}\n"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
+// acc += w (s, the columns' scales b where they differ), kN columns in pairs.
+template <bool kUniform, int kN>
+__device__ __forceinline__ void sum_columns(uint64_t* acc, const uint32_t (&w)[kN], const float4* b,
+                                            uint64_t s2) {
+#pragma unroll
+  for (int j = 0; j < kN / 4; ++j) {
+    uint64_t x = s2, y = s2;
+    if constexpr (!kUniform) {
+      x = mul2(pair(b[j].x, b[j].y), s2);
+      y = mul2(pair(b[j].z, b[j].w), s2);
+    }
+    acc[2 * j] = fma2(pair(w[4 * j], w[4 * j + 1]), x, acc[2 * j]);
+    acc[2 * j + 1] = fma2(pair(w[4 * j + 2], w[4 * j + 3]), y, acc[2 * j + 1]);
+  }
 }
 
 // Tile t: groups of kGroup tiles of A's rows, all of B's tiles within a group.
@@ -314,9 +315,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   using S = Shape<NT, kWide, kUniform>;
   constexpr int kBufs = S::kBufs, kStages = S::kStages, kSlots = S::kSlots;
   constexpr int kHalf = NT / 2;
+  constexpr int kG = S::kGroupBlocks;
   // columns in flight from tensor memory, twice (beside the sums, and the
   // columns' scales where they differ)
-  constexpr int kMostChunk = kUniform ? 32 : 16;
+  constexpr int kMostChunk = kWide && !kUniform ? 8 : 16;
   constexpr int kChunk = kHalf < kMostChunk ? kHalf : kMostChunk;
   extern __shared__ __align__(1024) uint8_t smem[];
 
@@ -424,27 +426,59 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ MMA issuer
     const uint32_t mine = elected();
     const uint64_t rows0 = desc_kmajor_sw128(smem_u32(sL)), cols0 = desc_kmajor_sw128(smem_u32(sC));
-    constexpr int kTurn = S::kTurn;
     bool ok = start_ok;
     int done = 0;
-    // phases at the start of a turn; within it they change as the rings wrap
-    for (uint32_t fphase = 0, tphase = 1; ok && done < blocks;
-         fphase ^= (kTurn / kStages) & 1, tphase ^= (kTurn / kBufs) & 1) {
+    if constexpr (kG == 1) {
+      constexpr int kTurn = S::kTurn;
+      // phases at the start of a turn; within it they change as the rings wrap
+      for (uint32_t fphase = 0, tphase = 1; ok && done < blocks;
+           fphase ^= (kTurn / kStages) & 1, tphase ^= (kTurn / kBufs) & 1) {
 #pragma unroll
-      for (int i = 0; i < kTurn; ++i) {
-        const int s = i % kStages, b = i % kBufs;
-        if (done >= blocks) break;
-        if (!mbar_wait_soon(smem_u32(&tempty[b]), tphase ^ ((i / kBufs) & 1), abort_flag, p.err) ||
-            !mbar_wait_soon(smem_u32(&full[s]), fphase ^ ((i / kStages) & 1), abort_flag, p.err)) {
-          ok = false;
-          break;
+        for (int i = 0; i < kTurn; ++i) {
+          const int s = i % kStages, b = i % kBufs;
+          if (done >= blocks) break;
+          if (!mbar_wait_soon(smem_u32(&tempty[b]), tphase ^ ((i / kBufs) & 1), abort_flag, p.err) ||
+              !mbar_wait_soon(smem_u32(&full[s]), fphase ^ ((i / kStages) & 1), abort_flag, p.err)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          umma_block(mine, tmem_base + b * NT, rows0 + s * (S::kLaneBytes >> 4),
+                     cols0 + s * (S::kColBytes >> 4), p.idesc);
+          commit(mine, smem_u32(&tfull[b]));
+          commit(mine, smem_u32(&empty[s]));
+          ++done;
         }
+      }
+    } else {
+      uint32_t s = 0, fphase = 0, b = 0, tphase = 1;
+      int kb = kb0;
+      while (ok && done < blocks) {
+        if (!mbar_wait_soon(smem_u32(&tempty[b]), tphase, abort_flag, p.err)) break;
         tc_fence_after();
-        umma_block(mine, tmem_base + b * NT, rows0 + s * (S::kLaneBytes >> 4),
-                   cols0 + s * (S::kColBytes >> 4), p.idesc);
+        const int n = min(kG, kb1 - kb);  // a tile's last group may be smaller
+        for (int i = 0; i < n; ++i) {
+          if (!mbar_wait_soon(smem_u32(&full[s]), fphase, abort_flag, p.err)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          umma_block(mine, tmem_base + (b * kG + i) * NT, rows0 + s * (S::kLaneBytes >> 4),
+                     cols0 + s * (S::kColBytes >> 4), p.idesc);
+          commit(mine, smem_u32(&empty[s]));
+          ++done;
+          if (++s == (uint32_t)kStages) {
+            s = 0;
+            fphase ^= 1u;
+          }
+        }
         commit(mine, smem_u32(&tfull[b]));
-        commit(mine, smem_u32(&empty[s]));
-        ++done;
+        kb += n;
+        if (kb == kb1) kb = kb0;
+        if (++b == (uint32_t)kBufs) {
+          b = 0;
+          tphase ^= 1u;
+        }
       }
     }
     // Every MMA this warp issued must be complete before TMEM is freed.
@@ -479,26 +513,31 @@ __global__ void __launch_bounds__(kThreads, 1)
           cs[i] = j < NT && row < p.col_n ? p.col_scale + (int64_t)row * p.col_sr : nullptr;
         }
       }
-      for (int kb = kb0; kb < kb1; ++kb) {
+      for (int kg = kb0; kg < kb1; kg += kG) {
         if (!mbar_wait_soon(smem_u32(&sempty[slot]), sphase ^ 1u, abort_flag, p.err)) {
           ok = false;
           break;
         }
-        const uint32_t dst = smem_u32(sS) + slot * S::kSlot;
 #pragma unroll
-        for (int i = 0; i < kLanes / 32; ++i)
-          copy4(dst + (i * 32 + lane) * 4, ls[i] ? ls[i] + kb * p.lane_sk : p.lane_scale,
-                ls[i] != nullptr);
-        if constexpr (kUniform) {
-          if (lane < NT / kBlock)
-            copy4(dst + (kLanes + lane) * 4, cs[0] ? cs[0] + kb * p.col_sk : p.col_scale,
-                  cs[0] != nullptr);
-        } else {
+        for (int g = 0; g < kG; ++g) {
+          const int kb = kg + g;
+          if (kb >= kb1) break;
+          const uint32_t dst = smem_u32(sS) + slot * S::kSlot + g * (S::kBlockScales * 4);
 #pragma unroll
-          for (int i = 0; i < (NT + 31) / 32; ++i)
-            if (i * 32 + lane < NT)
-              copy4(dst + (kLanes + i * 32 + lane) * 4, cs[i] ? cs[i] + kb * p.col_sk : p.col_scale,
-                    cs[i] != nullptr);
+          for (int i = 0; i < kLanes / 32; ++i)
+            copy4(dst + (i * 32 + lane) * 4, ls[i] ? ls[i] + kb * p.lane_sk : p.lane_scale,
+                  ls[i] != nullptr);
+          if constexpr (kUniform) {
+            if (lane < NT / kBlock)
+              copy4(dst + (kLanes + lane) * 4, cs[0] ? cs[0] + kb * p.col_sk : p.col_scale,
+                    cs[0] != nullptr);
+          } else {
+#pragma unroll
+            for (int i = 0; i < (NT + 31) / 32; ++i)
+              if (i * 32 + lane < NT)
+                copy4(dst + (kLanes + i * 32 + lane) * 4,
+                      cs[i] ? cs[i] + kb * p.col_sk : p.col_scale, cs[i] != nullptr);
+          }
         }
         copies_arrive(smem_u32(&sfull[slot]));
         if (++slot == kSlots) {
@@ -521,87 +560,119 @@ __global__ void __launch_bounds__(kThreads, 1)
       tile_coords<kWide>(p, t, tl, tc);
 #pragma unroll
       for (int j = 0; j < kHalf / 2; ++j) acc[j] = 0;
-      // The loads of a block's first columns are issued ahead, while the last
-      // columns of the block before are summed, where it is ready by then.
-      uint32_t r[2][kChunk];
-      float s = 0.f;
-      const float* sc = nullptr;
-      const uint32_t lane_addr = tmem_base + ((uint32_t)(quarter * 32) << 16) + half * kHalf;
-      auto begin = [&]() {  // the block at (slot, buf) is ready
-        tc_fence_after();
-        const float* sl = sS + slot * (S::kSlot / 4);
-        sc = sl + kLanes + (kUniform ? half : half * kHalf);
-        s = sl[quarter * 32 + lane];
-        if constexpr (kUniform) s *= sc[0];
-        tmem_ld<kChunk>(lane_addr + buf * NT, r[0]);
-      };
-      auto wait = [&]() {
-        return mbar_wait_soon(smem_u32(&sfull[slot]), sphase, abort_flag, p.err) &&
-               mbar_wait_soon(smem_u32(&tfull[buf]), bphase, abort_flag, p.err);
-      };
-      ok = kb0 < kb1 && wait();
-      if (!ok) break;
-      begin();
-      for (int kb = kb0; kb < kb1; ++kb) {
-        const uint64_t s2 = pair(s, s);
-        constexpr int kSteps = kHalf / kChunk;
-        static_assert(kSteps == 1 || kSteps % 2 == 0, "the next block starts in r[0]");
-        bool ahead = true;
-#pragma unroll
-        for (int c = 0; c < kSteps; ++c) {
-          uint32_t(&v)[kChunk] = r[c & 1];
-          float4 b[kUniform ? 1 : kChunk / 4];
-          if constexpr (!kUniform) {  // on their way while tensor memory answers
-#pragma unroll
-            for (int j = 0; j < kChunk / 4; ++j)
-              b[j] = *reinterpret_cast<const float4*>(sc + c * kChunk + 4 * j);
+      constexpr int kPer = kHalf / kChunk, kSteps = kG * kPer;
+      if constexpr (kG == 1) {
+        // a block at a time, the next 16 columns on their way while 16 are summed
+        uint32_t r[2][kChunk];
+        for (int kb = kb0; kb < kb1; ++kb) {
+          if (!mbar_wait_soon(smem_u32(&sfull[slot]), sphase, abort_flag, p.err)) {
+            ok = false;
+            break;
           }
-          tmem_wait<kChunk>(v);
-          if (c + 1 < kSteps) {
-            tmem_ld<kChunk>(lane_addr + buf * NT + (c + 1) * kChunk, r[(c + 1) & 1]);
-          } else {  // the block is in registers: its accumulator and scales are free
-            if constexpr (kSteps == 1) {
-#pragma unroll
-              for (int j = 0; j < kChunk; ++j) r[1][j] = r[0][j];
-            }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-              mbar_arrive(smem_u32(&tempty[buf]));
-              mbar_arrive(smem_u32(&sempty[slot]));
-            }
-            if (++slot == kSlots) {
-              slot = 0;
-              sphase ^= 1u;
-            }
-            if (++buf == kBufs) {
-              buf = 0;
-              bphase ^= 1u;
-            }
-            if (kb + 1 < kb1) {
-              ahead = __all_sync(0xFFFFFFFFu, mbar_test(smem_u32(&sfull[slot]), sphase) &&
-                                                  mbar_test(smem_u32(&tfull[buf]), bphase));
-              if (ahead) begin();
-            }
+          const float* sl = sS + slot * (S::kSlot / 4);
+          const float* sc = sl + kLanes + (kUniform ? half : half * kHalf);
+          float s = sl[quarter * 32 + lane];
+          if constexpr (kUniform) s *= sc[0];
+          const uint64_t s2 = pair(s, s);
+          if (!mbar_wait_soon(smem_u32(&tfull[buf]), bphase, abort_flag, p.err)) {
+            ok = false;
+            break;
           }
-          uint32_t(&w)[kChunk] = r[kSteps == 1 ? 1 : c & 1];
+          tc_fence_after();
+          const uint32_t taddr =
+              tmem_base + ((uint32_t)(quarter * 32) << 16) + buf * NT + half * kHalf;
+          tmem_ld<kChunk>(taddr, r[0]);
 #pragma unroll
-          for (int j = 0; j < kChunk / 4; ++j) {
-            uint64_t& a0 = acc[(c * kChunk + 4 * j) / 2];
-            uint64_t& a1 = acc[(c * kChunk + 4 * j) / 2 + 1];
-            if constexpr (kUniform) {
-              a0 = fma2(pair(w[4 * j], w[4 * j + 1]), s2, a0);
-              a1 = fma2(pair(w[4 * j + 2], w[4 * j + 3]), s2, a1);
-            } else {
-              a0 = fma2(pair(w[4 * j], w[4 * j + 1]), mul2(pair(b[j].x, b[j].y), s2), a0);
-              a1 = fma2(pair(w[4 * j + 2], w[4 * j + 3]), mul2(pair(b[j].z, b[j].w), s2), a1);
+          for (int c = 0; c < kPer; ++c) {
+            uint32_t(&w)[kChunk] = r[c & 1];
+            float4 b[kUniform ? 1 : kChunk / 4];
+            if constexpr (!kUniform) {  // on their way while tensor memory answers
+#pragma unroll
+              for (int j = 0; j < kChunk / 4; ++j)
+                b[j] = *reinterpret_cast<const float4*>(sc + c * kChunk + 4 * j);
             }
+            tmem_wait<kChunk>(w);
+            if (c + 1 < kPer) {
+              tmem_ld<kChunk>(taddr + (c + 1) * kChunk, r[(c + 1) & 1]);
+            } else {  // everything is in registers: the accumulator is free
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(smem_u32(&tempty[buf]));
+            }
+            sum_columns<kUniform, kChunk>(acc + c * kChunk / 2, w, b, s2);
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&sempty[slot]));
+          if (++slot == kSlots) {
+            slot = 0;
+            sphase ^= 1u;
+          }
+          if (++buf == kBufs) {
+            buf = 0;
+            bphase ^= 1u;
           }
         }
-        if (!ahead) {
-          ok = wait();
+      } else {
+        // A group's columns in steps of kChunk, two steps from tensor memory at a
+        // time: the next one is on its way while one is summed.
+        static_assert(kSteps % 2 == 0, "steps go in pairs");
+        uint32_t r[2][kChunk];
+        const uint32_t lane_addr = tmem_base + ((uint32_t)(quarter * 32) << 16) + half * kHalf;
+        for (int kb = kb0; kb < kb1; kb += kG) {
+          ok = mbar_wait_soon(smem_u32(&sfull[slot]), sphase, abort_flag, p.err) &&
+               mbar_wait_soon(smem_u32(&tfull[buf]), bphase, abort_flag, p.err);
           if (!ok) break;
-          begin();
+          tc_fence_after();
+          const int live = min(kG, kb1 - kb);  // blocks of the group
+          auto load = [&](int step) {
+            tmem_ld<kChunk>(lane_addr + (buf * kG + step / kPer) * NT + step % kPer * kChunk, r[step & 1]);
+          };
+          load(0);
+          load(1);
+          float sl[kG], sc[kUniform ? kG : 1];
+#pragma unroll
+          for (int g = 0; g < kG; ++g) {
+            const float* at = sS + slot * (S::kSlot / 4) + g * S::kBlockScales;
+            sl[g] = at[quarter * 32 + lane];
+            if constexpr (kUniform) sc[g] = at[kLanes + half];
+          }
+#pragma unroll
+          for (int st = 0; st < kSteps; ++st) {
+            const int g = st / kPer, c = st % kPer;
+            float4 b[kUniform ? 1 : kChunk / 4];
+            if constexpr (!kUniform) {  // on their way while tensor memory answers
+              const float* at = sS + slot * (S::kSlot / 4) + g * S::kBlockScales + kLanes + half * kHalf;
+#pragma unroll
+              for (int j = 0; j < kChunk / 4; ++j)
+                b[j] = *reinterpret_cast<const float4*>(at + c * kChunk + 4 * j);
+            }
+            if (st % 2 == 0) {
+              tmem_wait<kChunk>(r[0]);
+              tmem_tie<kChunk>(r[1]);
+              if (st + 2 >= kSteps) {  // the group is in registers
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&tempty[buf]));
+              }
+            }
+            if (g < live) {
+              const float s = kUniform ? sl[g] * sc[kUniform ? g : 0] : sl[g];
+              const uint64_t s2 = pair(s, s);
+              uint32_t(&w)[kChunk] = r[st & 1];
+              sum_columns<kUniform, kChunk>(acc + c * kChunk / 2, w, b, s2);
+            }
+            if (st + 2 < kSteps) load(st + 2);
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&sempty[slot]));
+          if (++slot == kSlots) {
+            slot = 0;
+            sphase ^= 1u;
+          }
+          if (++buf == kBufs) {
+            buf = 0;
+            bphase ^= 1u;
+          }
         }
       }
       if (!ok) break;
@@ -614,13 +685,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int n = tl * p.height + row;
         const int m0 = tc * NT + half * kHalf;
         const bool mine = row < p.height && n < p.N;
+        // the columns' 1 / tau, one a lane (a load for each column as it is
+        // written would be waited for each time)
+        float inv[(kHalf + 31) / 32];
 #pragma unroll
-        for (int j = 0; j < kHalf / 2; ++j) {
-          const float2 v = unpair(acc[j]);
-          if (m0 + 2 * j < p.M && mine)
-            finish<O>(p, m0 + 2 * j, n, v.x * over_tau(p, m0 + 2 * j));
-          if (m0 + 2 * j + 1 < p.M && mine)
-            finish<O>(p, m0 + 2 * j + 1, n, v.y * over_tau(p, m0 + 2 * j + 1));
+        for (int i = 0; i < (kHalf + 31) / 32; ++i) {
+          const int m = m0 + i * 32 + lane;
+          inv[i] = i * 32 + lane < kHalf && m < p.M ? over_tau(p, m) : 1.f;
+        }
+#pragma unroll
+        for (int j = 0; j < kHalf; ++j) {
+          if (m0 + j >= p.M) break;  // the same in every lane
+          const float2 v = unpair(acc[j / 2]);
+          const float x = (j % 2 ? v.y : v.x) * __shfl_sync(0xFFFFFFFFu, inv[j / 32], j % 32);
+          if (mine) finish<O>(p, m0 + j, n, x);
         }
       } else {
         // 32 rows x 64 bytes at a time: a thread's row in 16-byte pieces, piece
