@@ -577,11 +577,11 @@ __global__ void __launch_bounds__(kT, 1024 / kT) forward_kernel(const FwdArgs a)
       }
       __syncthreads();
     }
-    // Something above the bound (or at it while ties count), a NaN, or no bound
-    // yet: the warp looks at the thread's elements together, a lane each, in the
+    // Something above the bound (or at it while ties count; without one, above
+    // -inf), or a NaN: the warp looks at the thread's elements together, a lane each, in the
     // buffer (rare: about n elements for each doubling of the row). The thread
     // moves its base first.
-    const bool look = !(vmax < cut) && (equal || !bound || !(vmax <= cut));
+    const bool look = equal ? !(vmax < cut) : !(vmax <= cut);
     uint32_t lookers = __ballot_sync(0xFFFFFFFFu, look);
     if (lookers != 0u) {
       if (look) {
