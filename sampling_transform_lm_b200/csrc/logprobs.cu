@@ -471,14 +471,6 @@ __global__ void __launch_bounds__(kT, 1024 / kT) forward_kernel(const FwdArgs a)
   const int part = (int)((int64_t)blockIdx.x - row * parts);
   const int tid = threadIdx.x;
   const int n = max(a.n, 1);  // the first alternative gives the maximum
-  const float tau = a.tau ? a.tau[row] : 1.f;
-  const bool tau_ok = tau > 0.f && tau < INFINITY;
-  const double cd = exponent_scale(tau_ok ? tau : 1.f);
-  Factor c;
-  c.hi = (float)cd;
-  c.lo = (float)(cd - (double)c.hi);
-  c.far = true;  // until a maximum shows that it is not
-
   const int v0 = (int)min((int64_t)part * a.stretch, (int64_t)a.V);
   const int len = min(a.stretch, a.V - v0);
   const T* z = static_cast<const T*>(a.z) + row * a.ld + v0;
@@ -508,7 +500,14 @@ __global__ void __launch_bounds__(kT, 1024 / kT) forward_kernel(const FwdArgs a)
     fence_proxy_async_smem();
     for (int i = 0; i < min(kBuffers, chunks); ++i) order(i);
   }
+  const float tau = a.tau ? a.tau[row] : 1.f;  // on its way while the barriers are made
   __syncthreads();
+  const bool tau_ok = tau > 0.f && tau < INFINITY;
+  const double cd = exponent_scale(tau_ok ? tau : 1.f);
+  Factor c;
+  c.hi = (float)cd;
+  c.lo = (float)(cd - (double)c.hi);
+  c.far = true;  // until a maximum shows that it is not
 
   // the block's first given tokens and their logits, while the row arrives
   const T* zrow = static_cast<const T*>(a.z) + row * a.ld;
@@ -885,32 +884,56 @@ __global__ void __launch_bounds__(kThreads) backward_kernel(const BwdArgs a) {
   O* orow = static_cast<O*>(a.out) + row * a.out_ld;
   const T* z = zrow + v0;
   O* out = orow + v0;
-  const bool live = (a.flags[row] & (STS_ROW_INVALID | STS_ROW_EMPTY)) == 0;
+  const int head = min((int)((16u - (uint32_t)(reinterpret_cast<uintptr_t>(z) & 15u)) % 16u) /
+                           (int)sizeof(T), len);
+  const int body = (len - head) / kN;
+  const int tail0 = head + body * kN;
+  const T* zb = z + head;
+  O* ob = out + head;
+  constexpr uintptr_t kOutAlign = kN * sizeof(O) >= 16 ? 15u : 7u;
+  const bool vec_out = (reinterpret_cast<uintptr_t>(ob) & kOutAlign) == 0;
+
+  // what the row needs first is asked for at once, not one after the other: its
+  // scalars, its tokens and its first logits
+  const int32_t flags = a.flags[row];
+  const float tau_in = a.tau ? a.tau[row] : 1.f;
+  const float zmax = a.logit_max[row], log_sum = a.log_sum[row];
+  const double h = a.grad_entropy ? (double)a.grad_entropy[row] : 0.0;
+  const double entropy = a.grad_entropy ? (double)a.entropy[row] : 0.0;
+  Vec<T> v[kUnroll];
+  auto load = [&](int i0) {
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int i = i0 + u * kThreads + tid;
+      // not __ldg: the output may be the logits themselves
+      if (i < body) v[u].w = *reinterpret_cast<const uint4*>(zb + (int64_t)i * kN);
+    }
+  };
+  load(0);
+  const bool live = (flags & (STS_ROW_INVALID | STS_ROW_EMPTY)) == 0;
 
   // the tokens that get a share, with their logits: read before any block of
   // the row writes, since the gradient may take the logits' place
-  const int count = (a.grad ? a.m : 0) + (a.grad_top ? a.n : 0);
   const int given = a.grad ? a.m : 0;
+  const int count = given + (a.grad_top ? a.n : 0);
   double sum = 0.0;
-  if (live) {
-    for (int j = tid; j < count; j += kThreads) {
-      int64_t id;
-      float g;
-      if (j < given) {
-        id = a.tokens[row * a.tokens_ld + j];
-        g = a.grad[row * a.m + j];
-      } else {
-        id = a.top_id[row * a.n + (j - given)];
-        g = a.grad_top[row * a.n + (j - given)];
-      }
-      float zv = kNegInf;
-      if (id >= 0 && id < a.V) zv = to_f32(zrow[id]);
-      const bool valid = zv > kNegInf;
-      sm.id[j] = valid ? id : -1;
-      sm.g[j] = g;
-      sm.z[j] = zv;
-      if (valid) sum += (double)g;
+  for (int j = tid; j < count; j += kThreads) {
+    int64_t id;
+    float g;
+    if (j < given) {
+      id = a.tokens[row * a.tokens_ld + j];
+      g = a.grad[row * a.m + j];
+    } else {
+      id = a.top_id[row * a.n + (j - given)];
+      g = a.grad_top[row * a.n + (j - given)];
     }
+    float zv = kNegInf;
+    if (id >= 0 && id < a.V) zv = to_f32(zrow[id]);
+    const bool valid = zv > kNegInf;
+    sm.id[j] = valid ? id : -1;
+    sm.g[j] = g;
+    sm.z[j] = zv;
+    if (valid) sum += (double)g;
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
@@ -925,34 +948,18 @@ __global__ void __launch_bounds__(kThreads) backward_kernel(const BwdArgs a) {
   RowCoef k{0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   float tau = 1.f;
   if (live) {
-    tau = a.tau ? a.tau[row] : 1.f;
-    const double h = a.grad_entropy ? (double)a.grad_entropy[row] : 0.0;
-    k.zmax = a.logit_max[row];
+    tau = tau_in;
+    k.zmax = zmax;
     const double cd = exponent_scale(tau);
     k.c = (float)cd;
     k.lo = (float)(cd - (double)k.c);
-    k.l2s = (float)((double)a.log_sum[row] * kLog2eD);
-    k.a = (float)(-(sum + (h != 0.0 ? h * (double)a.entropy[row] : 0.0)) / (double)tau);
+    k.l2s = (float)((double)log_sum * kLog2eD);
+    k.a = (float)(-(sum + (h != 0.0 ? h * entropy : 0.0)) / (double)tau);
     k.b = (float)(-h * kLn2 / (double)tau);
   }
 
-  const int head = min((int)((16u - (uint32_t)(reinterpret_cast<uintptr_t>(z) & 15u)) % 16u) /
-                           (int)sizeof(T), len);
-  const int body = (len - head) / kN;
-  const int tail0 = head + body * kN;
-  const T* zb = z + head;
-  O* ob = out + head;
-  constexpr uintptr_t kOutAlign = kN * sizeof(O) >= 16 ? 15u : 7u;
-  const bool vec_out = (reinterpret_cast<uintptr_t>(ob) & kOutAlign) == 0;
-
   for (int i0 = 0; i0 < body; i0 += kThreads * kUnroll) {
-    Vec<T> v[kUnroll];
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int i = i0 + u * kThreads + tid;
-      // not __ldg: the output may be the logits themselves
-      if (live && i < body) v[u].w = *reinterpret_cast<const uint4*>(zb + (int64_t)i * kN);
-    }
+    if (i0 > 0) load(i0);
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       const int i = i0 + u * kThreads + tid;
