@@ -68,8 +68,6 @@ struct Shape {
   static constexpr uint32_t kColBytes = NT * kBlock;
   static constexpr uint32_t kStage = kLaneBytes + kColBytes;
   static constexpr int kStages = kWide ? (kUniform ? 4 : 3) : (NT == 128 ? 6 : 8);
-  // stages and accumulators repeat together after this many blocks
-  static constexpr int kTurn = kStages % kBufs == 0 ? kStages : kStages * kBufs;
   static constexpr int kSlots = 4;  // of a group's scales
   static constexpr int kColScales = kUniform ? 4 : NT;  // floats of a block's scales beyond the lanes' 128
   static constexpr uint32_t kBlockScales = kLanes + kColScales;
@@ -77,9 +75,12 @@ struct Shape {
   static constexpr uint32_t kStagingBytes = kWide ? kSumWarps * 2 * kStaging : 0;
   static constexpr int kBars = 2 * kStages + 2 * kSlots + 2 * kBufs + 1;
   static constexpr size_t kSmem = (size_t)kStages * kStage + kStagingBytes + kSlots * kSlot + kBars * 8 + 16;
-  static constexpr int kPitch = NT + 1;  // floats between rows of a split's sums
+  // a split's sums: a line for each m of C (wide: a lane, narrow: a column), n
+  // along it; 16 bytes more a line, against bank conflicts
+  static constexpr int kLines = kWide ? kLanes : NT, kLong = kWide ? NT : kLanes;
+  static constexpr int kPitch = kLong + 4;
   static_assert(kSmem <= 227 * 1024, "shared memory of one CTA");
-  static_assert((size_t)kStages * kStage >= (size_t)kLanes * kPitch * 4, "a split's sums fit the ring");
+  static_assert((size_t)kStages * kStage >= (size_t)kLines * kPitch * 4, "a split's sums fit the ring");
 };
 
 struct ProductArgs {
@@ -397,8 +398,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ operands
     const uint32_t mine = elected();
     const uint32_t bytes = (uint32_t)(p.height + NT) * kBlock;
-    int t = tile0, kb = kb0, tl, tc;
-    tile_coords<kWide>(p, t, tl, tc);
+    int t = tile0, kb = kb0, tl = 0, tc = 0;
+    if (t < tiles) tile_coords<kWide>(p, t, tl, tc);
     bool ok = start_ok;
     int done = 0;
     for (uint32_t phase = 1; ok && done < blocks; phase ^= 1u) {
@@ -415,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (++kb == kb1) {
           kb = kb0;
           t += step;
-          tile_coords<kWide>(p, t, tl, tc);
+          if (t < tiles) tile_coords<kWide>(p, t, tl, tc);
         }
       }
     }
@@ -429,7 +430,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = start_ok;
     int done = 0;
     if constexpr (kG == 1) {
-      constexpr int kTurn = S::kTurn;
+      // stages and accumulators repeat together after this many blocks
+      constexpr int kTurn = kStages % kBufs == 0 ? kStages : kStages * kBufs;
       // phases at the start of a turn; within it they change as the rings wrap
       for (uint32_t fphase = 0, tphase = 1; ok && done < blocks;
            fphase ^= (kTurn / kStages) & 1, tphase ^= (kTurn / kBufs) & 1) {
@@ -548,6 +550,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     asm volatile("cp.async.wait_all;" ::: "memory");  // before the CTA may exit
   }
+    if (p.split > 1) {  // the sums' exchange (below) has two of these
+      cg::this_cluster().sync();
+      cg::this_cluster().sync();
+    }
   } else {
     // ------------------------------------------------------------ scale and sum
     take_registers<kWide>();
@@ -763,42 +769,73 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     if (have) {
       // One tile per cluster. Every stage has been read by now (the sums wait
-      // for the last MMA), so the ring holds the sums, kPitch floats a lane.
-      float* mine = reinterpret_cast<float*>(smem) + (quarter * 32 + lane) * S::kPitch + half * kHalf;
+      // for the last MMA), so the ring holds the sums, a line for each m.
+      float* sums = reinterpret_cast<float*>(smem);
+      const int row = quarter * 32 + lane;
+      if constexpr (kWide) {
+        float4* mine = reinterpret_cast<float4*>(sums + row * S::kPitch + half * kHalf);
 #pragma unroll
-      for (int j = 0; j < kHalf / 2; ++j) {
-        const float2 v = unpair(acc[j]);
-        mine[2 * j] = v.x;
-        mine[2 * j + 1] = v.y;
-      }
-    }
-  }
-
-  if (p.split > 1) {
-    const float* sums = reinterpret_cast<const float*>(smem);
-    constexpr int kPitch = S::kPitch;
-    cg::cluster_group cluster = cg::this_cluster();
-    cluster.sync();
-    if (warp >= 4 && have) {
-      // the CTAs divide the lines that C's rows want written: one m, consecutive
-      // n (wide: a lane's sums; narrow: a column's)
-      constexpr int kLines = kWide ? kLanes : NT, kLong = kWide ? NT : kLanes;
-      for (int j = part + p.split * (warp - 4); j < kLines; j += p.split * kSumWarps) {
-        const int m = (kWide ? last_l * kLanes : last_c * NT) + j;
-        if (m >= p.M) break;
-        const float inv = over_tau(p, m);
-        const int n0 = kWide ? last_c * NT : last_l * p.height;
-        const int end = min(kWide ? kLong : p.height, p.N - n0);
-        for (int i = lane; i < end; i += 32) {
-          const int at = kWide ? j * kPitch + i : i * kPitch + j;
-          float v = 0.f;
-          for (int q = 0; q < p.split; ++q) v += cluster.map_shared_rank(sums, q)[at];
-          finish<O>(p, m, n0 + i, v * inv);
+        for (int j = 0; j < kHalf / 4; ++j) {
+          const float2 x = unpair(acc[2 * j]), y = unpair(acc[2 * j + 1]);
+          mine[j] = make_float4(x.x, x.y, y.x, y.y);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < kHalf / 2; ++j) {
+          const float2 v = unpair(acc[j]);
+          sums[(half * kHalf + 2 * j) * S::kPitch + row] = v.x;
+          sums[(half * kHalf + 2 * j + 1) * S::kPitch + row] = v.y;
         }
       }
     }
-    cluster.sync();
+    if (p.split > 1) {
+      float* sums = reinterpret_cast<float*>(smem);
+      cg::cluster_group cluster = cg::this_cluster();
+      cluster.sync();
+      if (have) {
+        // the CTAs divide the lines; the parts are added in the order of k
+        const float* from[kMaxSplit];
+#pragma unroll
+        for (int q = 0; q < kMaxSplit; ++q)
+          from[q] = cluster.map_shared_rank(sums, q < p.split ? q : 0);
+        for (int j = part + p.split * (warp - 4); j < S::kLines; j += p.split * kSumWarps) {
+          const int m = (kWide ? last_l * kLanes : last_c * NT) + j;
+          if (m >= p.M) break;
+          const float inv = over_tau(p, m);
+          const int n0 = kWide ? last_c * NT : last_l * p.height;
+          const int end = min(kWide ? S::kLong : p.height, p.N - n0);
+          // a line's pieces from every part are on their way before one is added
+          constexpr int kSteps = S::kLong / 128;
+          float4 x[kSteps][kMaxSplit];
+#pragma unroll
+          for (int t = 0; t < kSteps; ++t)
+#pragma unroll
+            for (int q = 0; q < kMaxSplit; ++q)
+              if (q < p.split)
+                x[t][q] = *reinterpret_cast<const float4*>(from[q] + j * S::kPitch + t * 128 + lane * 4);
+#pragma unroll
+          for (int t = 0; t < kSteps; ++t) {
+            float v[4] = {x[t][0].x, x[t][0].y, x[t][0].z, x[t][0].w};
+#pragma unroll
+            for (int q = 1; q < kMaxSplit; ++q) {
+              if (q < p.split) {
+                v[0] += x[t][q].x;
+                v[1] += x[t][q].y;
+                v[2] += x[t][q].z;
+                v[3] += x[t][q].w;
+              }
+            }
+            const int i = t * 128 + lane * 4;
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+              if (i + u < end) finish<O>(p, m, n0 + i + u, v[u] * inv);
+          }
+        }
+      }
+      cluster.sync();
+    }
   }
+
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
@@ -849,6 +886,21 @@ cudaError_t launch_out(int NT, bool uniform, const Maps& maps, const ProductArgs
 }
 
 constexpr int64_t kMost = (int64_t(1) << 31) - 1024;
+
+// Which form. Above 128 rows of A the wide one, up to 64 the narrow one; between
+// them by the rounds of tiles that each takes over the SMs. A round of the wide
+// form's tiles takes about as long as its blocks along k and 12 more (its results
+// leave while nothing is multiplied), of the narrow form's as its blocks and 2
+// more. 70 x 21,000 x 4,096: wide 33 us, narrow 51; 100 x 151,936 x 4,096: 145
+// and 207; 77 x 50,021 x 2,048: 57 and 47; 128 x 2,048 x 2,048: 27 and 21.
+bool wide_form(int64_t M, int64_t N, int64_t kb, int sms) {
+  if (M > 128) return true;
+  if (M <= 64) return false;
+  const int64_t wide = ((N + 255) / 256 + sms - 1) / sms;
+  const int64_t narrow = (N + (int64_t)kLanes * sms - 1) / ((int64_t)kLanes * sms);
+  return wide * (kb + 12) < narrow * (kb + 2);
+}
+
 constexpr int kMinHeight = 16;  // rows of B in the narrow form's smallest tile
 
 sts_status check_operand(const sts_block_operand* o, int64_t K, bool rows_only) {
@@ -896,7 +948,7 @@ extern "C" sts_status sts_block_scaled_product(const sts_block_operand* A,
   if (s != STS_OK) return s;
 
   const int64_t M = A->rows, N = B->rows;
-  const bool wide = M > kLanes;
+  const bool wide = wide_form(M, N, (K + kBlock - 1) / kBlock, sms);
   const int NT = wide ? 256 : M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
   const sts_block_operand* L = wide ? A : B;  // the lanes' operand
   const sts_block_operand* R = wide ? B : A;  // the columns'
