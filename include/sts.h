@@ -398,9 +398,9 @@ typedef struct {
 /* C [M, N] = A [M, K] . B [N, K]^T, each block of 128 along K scaled in fp32:
  *   C[m, n] = sum_kb a[m, kb] b[n, kb] sum_{k in kb} A[m, k] B[n, k]
  * (tensor-core products and sums of a block in fp32, blocks summed in fp32
- * registers in increasing k), then divided by temperature[m] where that is
- * given (IEEE fp32 division, not validated: sts_resolve_logits and
- * sts_token_logprobs check the rows' temperatures), then added to C where
+ * registers in increasing k), then multiplied by 1 / temperature[m] where that
+ * is given (the reciprocal rounded to fp32; not validated: sts_resolve_logits
+ * and sts_token_logprobs check the rows' temperatures), then added to C where
  * accumulate is set (fp32 C only), then rounded to c_dtype (STS_DTYPE_F32 or
  * _BF16). With the hidden states as A and a head [V, d] as B it is the 8-bit
  * counterpart of sts_scaled_logits; the logits' gradient as A and the
@@ -452,9 +452,12 @@ typedef struct {
  *     -inf, entropy 0, no alternatives.
  *   - A row with a bad temperature, a token outside [-1, V), or a logit that is
  *     NaN or +inf is invalid: its floating results are NaN, its ids -1, its
- *     flags say why; other rows are unaffected. There is no status word.
- * Sums in fp32 per thread, joined in float64. Asynchronous, allocates nothing,
- * one kernel launch; calls share nothing and may overlap. T = 0 is allowed. */
+ *     flags say why; other rows are unaffected. There is no status word (a
+ *     device-side wait that gave up shows as STS_ROW_BAD_LOGIT).
+ * Sums in fp32 per thread, joined in float64; 16-bit logits are multiplied by
+ * log2(e) / tau rounded to fp32, fp32 logits by two parts of it. Asynchronous,
+ * allocates nothing, one kernel launch; calls share nothing and may overlap.
+ * T = 0 is allowed. */
 sts_status sts_token_logprobs(const sts_token_rows* rows, float* logprob,
                               const sts_token_stats* stats, sts_stream_t stream);
 
@@ -469,7 +472,8 @@ sts_status sts_token_logprobs(const sts_token_rows* rows, float* logprob,
  * read, entropy where grad_entropy is given, top_id where grad_top is.
  * dlogits [T][dlogits_ld] in STS_DTYPE_F32, _BF16 or _F16 (entries past V are
  * left as they are); it may be the logits themselves (same pointer, type and
- * stride), not a part of them (STS_ERR_SHAPE). Asynchronous, allocates nothing,
+ * stride), and may not otherwise lie between their first and last element
+ * (STS_ERR_SHAPE). Asynchronous, allocates nothing,
  * one kernel launch. */
 sts_status sts_token_logprobs_backward(const sts_token_rows* rows, const sts_token_stats* saved,
                                        const float* grad_logprob, const float* grad_entropy,

@@ -919,8 +919,8 @@ def sts_block_scaled_product(A, a_scale, B, b_scale, *, temperature=None, out=No
     """C [M, N] = A [M, K] . B [N, K]^T of 8-bit matrices with their scales (``sts_block_quantize``):
     ``a_scale`` [M, ceil(K / 128)], ``b_scale`` [N, ceil(K / 128)] or [ceil(N / 128), ceil(K / 128)].
 
-    Each block of 128 is summed on the tensor cores and scaled in fp32. The rows are divided by
-    ``temperature`` [M] where it is given (the scaled logits of an 8-bit head). C is ``out`` or new,
+    Each block of 128 is summed on the tensor cores and scaled in fp32. The rows are multiplied by
+    1 / ``temperature`` [M] where it is given (the scaled logits of an 8-bit head). C is ``out`` or new,
     fp32 (default) or bf16; with ``accumulate`` the product is added to ``out`` (fp32). With
     ``check`` the call synchronises and raises if a device-side wait gave up."""
     lib = load()

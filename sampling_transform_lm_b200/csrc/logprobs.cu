@@ -43,6 +43,15 @@
 // GPU, that of a cluster of 2, 4 or 8 blocks, each with a stretch of the
 // vocabulary; the first block joins their results over distributed shared
 // memory. One launch, no workspace, nothing shared between calls.
+//
+// What it takes. The gradient: 4,096 rows of 152,064 bf16 logits 397 us, 6.27
+// TB/s, 96 % of a measured copy. The forward: the same rows 281 us without
+// alternatives, 307 with 8, 453 with 64 (HBM: 190); 2,048 rows of 151,936 fp32 with
+// 20 270 (190). It issues 2.7 to 3 instructions a clock (some 10 an element, and
+// one exponential, which alone would take as long as the bytes do); 64
+// alternatives cost 2,400 instructions a row and warp more, in ranking them at
+// each doubling of the row. Packed fp32 operations lost more in moves than they
+// saved, loads by registers waited for memory, and a prefetch of them spilled.
 #include <cmath>
 #include <type_traits>
 

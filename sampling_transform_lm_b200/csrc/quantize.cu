@@ -25,6 +25,11 @@
 //   cols     x's rows are contiguous (a transposed view): 256 threads hold 128
 //            x 128 elements; the codes cross shared memory, so that both the
 //            reads along x's rows and the writes along K are whole lines.
+// 151,936 x 4,096 bf16 takes 330 us in either block (5.7 TB/s, 86 % of a measured
+// copy), fp32 32,768 x 4,096 107 us (6.3 TB/s); rows that are no multiple of 16
+// bytes are read element by element (32,768 x 4,001 fp32: 168 us). cols holds two
+// to three thread blocks an SM, too few to hide its three barriers: 32,768 x
+// 4,001 bf16, transposed, 93 us (4.2 TB/s).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>

@@ -154,7 +154,11 @@ PRODUCTS = [  # M, N, K, a, b, b_rows, out, tau
     (64, 2048, 4096, E4M3, E4M3, 128, "fp32", True),
     (77, 30011, 640, E4M3, E4M3, 128, "bf16", True),
     (100, 1027, 777, E5M2, E5M2, 1, "fp32", False),
+    (70, 21000, 700, E4M3, E4M3, 128, "fp32", True),  # 65 to 128 rows: the wide form
+    (90, 300, 4000, E4M3, E4M3, 128, "bf16", True),  # and the narrow one, split over k
+    (128, 5000, 129, E5M2, E4M3, 1, "fp32", False),
     (129, 1024, 1025, E4M3, E4M3, 128, "fp32", True),
+    (200, 300, 9000, E4M3, E4M3, 1, "bf16", True),  # wide, split over k
     (256, 4000, 300, E4M3, E4M3, 1, "bf16", False),
     (1000, 777, 2047, E5M2, E4M3, 1, "fp32", True),
     (4500, 1500, 512, E4M3, E4M3, 128, "fp32", False),  # more than one raster group
@@ -199,6 +203,38 @@ def test_product_strides_accumulation_and_neighbours(cuda_lib, M, N, K):
     rest = held.clone()
     rest[1:-1, 1:N + 1] = 5.0
     assert (rest == 5.0).all()
+
+
+@pytest.mark.parametrize("M,N,K", [(40, 300, 9000), (300, 400, 9000)])
+def test_product_split_over_k_accumulates_and_fits_any_rows(cuda_lib, M, N, K):
+    """A cluster per tile, both forms: C off any alignment, added to, its neighbours left alone."""
+    gen = torch.Generator().manual_seed(9)
+    A, sa = _operand(gen, M, K, E4M3, 1)
+    B, sb = _operand(gen, N, K, E4M3, 128)
+    held = torch.full((M, N + 3), 5.0, device="cuda")
+    cuda_lib.sts_block_scaled_product(A, sa, B, sb, out=held[:, 1:N + 1], accumulate=True)
+    want, size = _product_reference(A, sa, B, sb, 128)
+    err = (held[:, 1:N + 1].double() - 5 - want).abs()
+    assert (err <= _product_tol(want, size, K, torch.float32) + 2 * U * (5 + want.abs())).all()
+    assert (held[:, 0] == 5).all() and (held[:, N + 1:] == 5).all()
+
+
+def test_far_offsets(cuda_lib):
+    """Elements beyond 2^31, of the source, the codes and the product."""
+    R, K = 540000, 4096
+    x = torch.zeros(R, K, dtype=torch.bfloat16, device="cuda")
+    x[-3:] = torch.randn(3, K, device="cuda").bfloat16()
+    for block_rows in (1, 128):
+        q, s = cuda_lib.sts_block_quantize(x, block_rows=block_rows)
+        want_q, want_s = quantize_reference(x[-96:], block_rows, E4M3)  # 540,000 = 128 * 4218 + 96
+        _same_codes(q[-96:], want_q)
+        assert torch.equal(s[-want_s.shape[0]:].cpu(), want_s)
+    A, sa = cuda_lib.sts_block_quantize(torch.randn(4200, 128, device="cuda"))
+    B, sb = q[:, :128].contiguous(), s[:, :1].contiguous()
+    C = cuda_lib.sts_block_scaled_product(A, sa, B, sb)
+    assert C.numel() > 2 ** 31
+    assert torch.equal(C[-5:, -3:], cuda_lib.sts_block_scaled_product(A[-5:], sa[-5:], B, sb)[:, -3:])
+    assert (C[-1, :-3] == 0).all() and (C[-1, -3:] != 0).all()
 
 
 def test_product_not_finite(cuda_lib):

@@ -379,6 +379,43 @@ def test_repeats_streams_and_graphs(cuda_lib):
         assert torch.equal(a, b)
 
 
+def test_far_offsets(cuda_lib):
+    """Rows beyond 2^31 elements: the same results as on their own."""
+    sts = cuda_lib
+    T, V = 15000, 152064
+    z = torch.zeros(T, V, dtype=torch.bfloat16, device="cuda")
+    z[-700:] = (torch.randn(700, V, device="cuda") * 3).bfloat16()
+    tokens = torch.randint(V, (T, 2), device="cuda")
+    lp, saved = sts.sts_token_logprobs(z, tokens, top_n=5, entropy=True)
+    few, part = sts.sts_token_logprobs(z[-700:], tokens[-700:], top_n=5, entropy=True)
+    assert torch.equal(lp[-700:], few)
+    for k, v in part.items():
+        assert torch.equal(saved[k][-700:], v), k
+    g = torch.randn(T, 2, device="cuda")
+    want = sts.sts_token_logprobs_backward(z[-700:], tokens[-700:], part, g[-700:])
+    assert torch.equal(sts.sts_token_logprobs_backward(z, tokens, saved, g, out=z)[-700:], want)
+
+
+def test_calls_that_overlap(cuda_lib):
+    """Forward and gradient calls on several streams at once, as independent calls."""
+    sts = cuda_lib
+    T, V = 6, 60000
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    rows = [_rows(20 + i, T, V, "bf16")[0].cuda() for i in range(3)]
+    tokens = torch.randint(V, (T, 2), device="cuda")
+    g = torch.randn(T, 2, device="cuda")
+    torch.cuda.synchronize()
+    got = []
+    for z, st in zip(rows, streams):
+        lp, s = sts.sts_token_logprobs(z, tokens, top_n=9, entropy=True, stream=st)
+        got.append((lp, s, sts.sts_token_logprobs_backward(z, tokens, s, g, stream=st)))
+    torch.cuda.synchronize()
+    for z, (lp, s, dz) in zip(rows, got):
+        lp1, s1 = sts.sts_token_logprobs(z, tokens, top_n=9, entropy=True)
+        assert torch.equal(lp, lp1) and torch.equal(s["top_id"], s1["top_id"]) and torch.equal(s["entropy"], s1["entropy"])
+        assert torch.equal(dz, sts.sts_token_logprobs_backward(z, tokens, s1, g))
+
+
 def test_no_rows(cuda_lib):
     z = torch.empty(0, 50, device="cuda")
     lp, saved = cuda_lib.sts_token_logprobs(z, torch.empty(0, 2, dtype=torch.int64, device="cuda"), top_n=2)
