@@ -804,38 +804,31 @@ __global__ void __launch_bounds__(kThreads, 1)
       cluster.sync();
       if (have) {
         // the CTAs divide the lines; the parts are added in the order of k
-        const float* from[kMaxSplit];
-#pragma unroll
-        for (int q = 0; q < kMaxSplit; ++q)
-          from[q] = cluster.map_shared_rank(sums, q < p.split ? q : 0);
         for (int j = part + p.split * (warp - 4); j < S::kLines; j += p.split * kSumWarps) {
           const int m = (kWide ? last_l * kLanes : last_c * NT) + j;
           if (m >= p.M) break;
           const float inv = over_tau(p, m);
           const int n0 = kWide ? last_c * NT : last_l * p.height;
           const int end = min(kWide ? S::kLong : p.height, p.N - n0);
-          // a line's pieces from every part are on their way before one is added
-          constexpr int kSteps = S::kLong / 128;
-          float4 x[kSteps][kMaxSplit];
-#pragma unroll
-          for (int t = 0; t < kSteps; ++t)
+          // 128 elements of a line; what every part has of them is on its way
+          // before the first is added
+#pragma unroll 1
+          for (int i = lane * 4; i < S::kLong; i += 128) {
+            float4 x[kMaxSplit];
 #pragma unroll
             for (int q = 0; q < kMaxSplit; ++q)
               if (q < p.split)
-                x[t][q] = *reinterpret_cast<const float4*>(from[q] + j * S::kPitch + t * 128 + lane * 4);
-#pragma unroll
-          for (int t = 0; t < kSteps; ++t) {
-            float v[4] = {x[t][0].x, x[t][0].y, x[t][0].z, x[t][0].w};
+                x[q] = *reinterpret_cast<const float4*>(cluster.map_shared_rank(sums, q) + j * S::kPitch + i);
+            float v[4] = {x[0].x, x[0].y, x[0].z, x[0].w};
 #pragma unroll
             for (int q = 1; q < kMaxSplit; ++q) {
               if (q < p.split) {
-                v[0] += x[t][q].x;
-                v[1] += x[t][q].y;
-                v[2] += x[t][q].z;
-                v[3] += x[t][q].w;
+                v[0] += x[q].x;
+                v[1] += x[q].y;
+                v[2] += x[q].z;
+                v[3] += x[q].w;
               }
             }
-            const int i = t * 128 + lane * 4;
 #pragma unroll
             for (int u = 0; u < 4; ++u)
               if (i + u < end) finish<O>(p, m, n0 + i + u, v[u] * inv);

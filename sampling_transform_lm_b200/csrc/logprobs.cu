@@ -868,6 +868,52 @@ __device__ __forceinline__ void store_vec(O* p, const float (&v)[kN]) {
   }
 }
 
+// The same where the output's 16-byte boundaries lie `skip` bytes into each
+// lane's 16 bytes (the same in every lane): a lane stores the 16 bytes from its
+// own boundary on, the rest of its vector and the start of the next lane's; the
+// first lane's start and the last one's rest go element by element. Every lane
+// of the warp calls it; `mine`: it has a vector (those that have come first).
+template <typename O, int kN>
+__device__ __forceinline__ void store_shifted(O* p, const float (&v)[kN], int skip, bool mine) {
+  static_assert(kN * sizeof(O) == 16, "16 bytes a lane");
+  union {
+    O o[kN];
+    uint32_t w[4];
+  } u;
+#pragma unroll
+  for (int i = 0; i < kN; ++i) from_f32(v[i], u.o[i]);
+  uint32_t c[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    c[i] = u.w[i];
+    c[i + 4] = __shfl_down_sync(0xFFFFFFFFu, u.w[i], 1);
+  }
+  const int lane = (int)threadIdx.x & 31;
+  const bool next = __shfl_down_sync(0xFFFFFFFFu, mine ? 1 : 0, 1) != 0 && lane < 31;
+  if (!mine) return;
+  if (next) {
+    const int bits = (skip & 3) * 8;
+    uint32_t d[5];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) {
+      const uint32_t lo = (skip & 4) ? c[i + 1 < 8 ? i + 1 : 7] : c[i];
+      const uint32_t hi = (skip & 4) ? c[i + 3 < 8 ? i + 3 : 7] : c[i + 2];
+      d[i] = (skip & 8) ? hi : lo;
+    }
+    uint4 w;
+    w.x = __funnelshift_r(d[0], d[1], bits);
+    w.y = __funnelshift_r(d[1], d[2], bits);
+    w.z = __funnelshift_r(d[2], d[3], bits);
+    w.w = __funnelshift_r(d[3], d[4], bits);
+    *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(p) + skip) = w;
+  }
+#pragma unroll
+  for (int i = 0; i < kN; ++i) {
+    const bool start = i * (int)sizeof(O) < skip;
+    if (start ? lane == 0 : !next) p[i] = u.o[i];
+  }
+}
+
 struct RowCoef {
   float zmax, c, lo, l2s;  // x = (z - zmax) (c + lo) - l2s, p = 2^x
   float a, b;              // dz = p (a + b x)
@@ -880,7 +926,7 @@ __device__ __forceinline__ float grad_of(float z, const RowCoef& k) {
 }
 
 template <typename T, typename O>
-__global__ void __launch_bounds__(kThreads) backward_kernel(const BwdArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) backward_kernel(const BwdArgs a) {
   __shared__ BwdSmem sm;
   constexpr int kN = Vec<T>::kN;
   const int parts = a.parts;
@@ -901,6 +947,7 @@ __global__ void __launch_bounds__(kThreads) backward_kernel(const BwdArgs a) {
   O* ob = out + head;
   constexpr uintptr_t kOutAlign = kN * sizeof(O) >= 16 ? 15u : 7u;
   const bool vec_out = (reinterpret_cast<uintptr_t>(ob) & kOutAlign) == 0;
+  const int skip = (int)((16u - (uint32_t)(reinterpret_cast<uintptr_t>(ob) & 15u)) & 15u);
 
   // what the row needs first is asked for at once, not one after the other: its
   // scalars, its tokens and its first logits
@@ -972,23 +1019,23 @@ __global__ void __launch_bounds__(kThreads) backward_kernel(const BwdArgs a) {
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       const int i = i0 + u * kThreads + tid;
-      if (i < body) {
-        float f[kN];
-        if (live) {
-          v[u].f32(f);
+      if (i - (tid & 31) >= body) break;  // no lane of the warp has one
+      float f[kN];
 #pragma unroll
-          for (int j = 0; j < kN; ++j) f[j] = grad_of(f[j], k);
-        } else {
+      for (int j = 0; j < kN; ++j) f[j] = 0.f;
+      if (live && i < body) {
+        v[u].f32(f);
 #pragma unroll
-          for (int j = 0; j < kN; ++j) f[j] = 0.f;
-        }
-        O* p = ob + (int64_t)i * kN;
-        if (vec_out) {
-          store_vec<O, kN>(p, f);
-        } else {
+        for (int j = 0; j < kN; ++j) f[j] = grad_of(f[j], k);
+      }
+      O* p = ob + (int64_t)i * kN;
+      if (vec_out) {
+        if (i < body) store_vec<O, kN>(p, f);
+      } else if constexpr (sizeof(O) == sizeof(T)) {
+        store_shifted<O, kN>(p, f, skip, i < body);
+      } else if (i < body) {
 #pragma unroll
-          for (int j = 0; j < kN; ++j) from_f32(f[j], p[j]);
-        }
+        for (int j = 0; j < kN; ++j) from_f32(f[j], p[j]);
       }
     }
   }
