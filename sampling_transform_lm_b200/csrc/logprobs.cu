@@ -1064,13 +1064,33 @@ __global__ void __launch_bounds__(kThreads, 4) backward_kernel(const BwdArgs a) 
 
 // ---------------------------------------------------------------- launches
 
-// Parts per row: as many as it takes to give every SM `want` blocks, at most 8,
-// and none shorter than one round of the loop.
-int parts_for(int64_t T, int64_t V, int elem, int sms, int threads) {
+// Parts per row: 1, 2, 4 or 8, none much shorter than one round of the loop; a
+// block's cost is its bytes and 32 KB more. The gradient and the forward's short
+// rows: as many waves of blocks as there are, four (of 128 threads seven) an SM:
+// 700 rows of 152,064 bf16, gradient, 2 parts 90 us, 1 part 102; 400 rows 1 part
+// 57, 2 parts 61; 333 rows of 32,771 fp32, forward, 2 parts 39, 4 parts 53. The
+// forward's long rows are bound by instructions: as many blocks as the busiest SM
+// gets, the slower the fewer threads that SM has: 100 rows of 152,064 bf16 4 parts
+// 29 us, 8 parts 37; 400 rows 2 parts 57, 1 part 70; 700 rows 1 part 78, 2 parts 109.
+int parts_for(int64_t T, int64_t V, int elem, int sms, int threads, bool forward) {
   const int64_t round = (int64_t)threads * kUnroll * (16 / elem);
-  int parts = 1;
-  while (parts < kMaxParts && T * parts < (int64_t)sms * 4 && V > round * parts) parts *= 2;
-  return parts;
+  int best = 1;
+  double least = 0.0;
+  for (int parts = 1; parts <= kMaxParts && (parts == 1 || V > round * (parts / 2)); parts *= 2) {
+    const bool busiest = forward && threads == 256;
+    const int64_t slots = busiest ? sms : (int64_t)sms * (threads == 128 ? 7 : 4);
+    const int64_t turns = (T * parts + slots - 1) / slots;
+    double cost = (double)turns * ((double)V * elem / parts + 32768.0);
+    if (busiest) {
+      const int64_t held = turns * threads;  // threads of the busiest SM
+      cost /= held >= 1024 ? 1.0 : held >= 768 ? 0.9 : held >= 512 ? 0.7 : 0.4;
+    }
+    if (parts == 1 || cost < least) {
+      best = parts;
+      least = cost;
+    }
+  }
+  return best;
 }
 
 template <typename K, typename A>
@@ -1149,7 +1169,7 @@ extern "C" sts_status sts_token_logprobs(const sts_token_rows* rows, float* logp
   a.T = rows->T;
   a.V = (int)rows->V;
   const int threads = rows->V <= kShortRow ? 128 : 256;
-  a.parts = parts_for(rows->T, rows->V, elem_size(rows->dtype), sms, threads);
+  a.parts = parts_for(rows->T, rows->V, elem_size(rows->dtype), sms, threads, true);
   a.stretch = (int)(((rows->V + a.parts - 1) / a.parts + 63) / 64 * 64);
   a.tokens = rows->tokens;
   a.tokens_ld = rows->tokens_ld;
@@ -1221,7 +1241,7 @@ extern "C" sts_status sts_token_logprobs_backward(const sts_token_rows* rows,
   a.ld = rows->ld;
   a.T = rows->T;
   a.V = (int)rows->V;
-  a.parts = parts_for(rows->T, rows->V, es, sms, kThreads);
+  a.parts = parts_for(rows->T, rows->V, es, sms, kThreads, false);
   a.stretch = (int)(((rows->V + a.parts - 1) / a.parts + 63) / 64 * 64);
   a.tokens = rows->tokens;
   a.tokens_ld = rows->tokens_ld;
