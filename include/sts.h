@@ -35,7 +35,8 @@
  *     gradient; other rows are unaffected.
  *   - A target outside its row's support is not an error: logprob = -inf
  *     and the row's gradient is zero (item 4 of the page).
- *   - Only bf16 H and W are accepted (an fp8 head is rejected one level up,
+ *   - Only bf16 H and W are accepted by the core (a head kept in 8 bits has
+ *     entry points of its own, sts_block_*; here it is rejected one level up,
  *     in the Python binding, with STS_ERR_DTYPE).
  *   - Layouts: H [T, d] and W [V, d] row-major bf16 (nn.Linear weight
  *     layout); dH [T, d] and dW [V, d] row-major fp32; per-row arrays [T].
