@@ -862,14 +862,15 @@ def sts_block_quantize(x, *, block_rows=1, dtype=_E4M3, q=None, scale=None, stre
         raise StsError(STS_ERR_SHAPE, f"block_rows must be 1 or {_BLOCK}, got {block_rows}")
     R, K = x.shape
     sr, sk = x.stride()
-    if K == 1 or (R > 1 and sk != 1 and sr != 1):
-        # one column is a row-contiguous matrix of any row stride
-        if K != 1:
-            raise StsError(STS_ERR_SHAPE, "x must have unit stride along its rows or columns")
+    if K == 1:  # one column: rows of any stride but 0
         sk = 1
-        sr = max(sr, 1)
-    elif R == 1 and sk != 1:
-        sr = 1  # one row of strided columns: a transposed view
+        if R == 1:
+            sr = 1
+    elif R == 1 and sk != 1:  # one row of strided columns: a transposed view
+        sr = 1
+    if (sk != 1 and sr != 1) or (R > 1 and sr < 1) or (K > 1 and sk < 1):
+        raise StsError(STS_ERR_SHAPE, "x must have unit stride along its rows or its columns, and no "
+                                      f"stride of 0: {x.stride()}")
     index, elsewhere = _place(stream, (("x", x), ("q", q), ("scale", scale)))
     if elsewhere is not None:
         with elsewhere:

@@ -117,6 +117,10 @@ def test_binding_refusals():
     assert e.value.status == DTYPE
     with pytest.raises(sts.StsError):
         sts.sts_block_quantize(bf[:, ::2][::2])
+    for view in (torch.ones(1, 1).expand(5, 1), torch.ones(1, 4).expand(5, 4), torch.ones(4, 1).expand(4, 5)):
+        with pytest.raises(sts.StsError) as e:  # a broadcast view has nothing behind its rows
+            sts.sts_block_quantize(view)
+        assert e.value.status == SHAPE and ("stride" in str(e.value) or "CUDA" in str(e.value))
     q = bf.to(torch.float8_e4m3fn)
     s = torch.ones(4, 2)
     for a, sa, b, sb, status in ((bf, s, q, s, DTYPE), (q, s[:3], q, s, SHAPE), (q, s, q, s[:, :1], SHAPE), (q, s.double(), q, s, DTYPE),

@@ -93,6 +93,15 @@ def test_quantize_layouts(cuda_lib):
     assert (raw[:, :3] == 9).all() and (raw[:, 303:] == 9).all() and (s[:, :2] == -1).all() and (s[:, 5:] == -1).all()
 
 
+def test_quantize_refuses_broadcast_views_and_takes_no_rows(cuda_lib):
+    one = torch.ones(4, 1, device="cuda")
+    for view in (one[:1].expand(5, 1), torch.ones(1, 4, device="cuda").expand(5, 4), one.expand(4, 5)):
+        with pytest.raises(cuda_lib.StsError):
+            cuda_lib.sts_block_quantize(view)
+    q, s = cuda_lib.sts_block_quantize(torch.empty(0, 200, device="cuda"))
+    assert q.shape == (0, 200) and s.shape == (0, 2)
+
+
 def test_quantize_values_at_the_edges(cuda_lib):
     """Zero blocks, NaN and infinities, subnormals, the largest finite values, exact ties."""
     x = torch.zeros(9, 256)
