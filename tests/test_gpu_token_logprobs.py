@@ -184,6 +184,31 @@ def test_hard_rows(cuda_lib, dtype, V, copies):
     assert torch.equal(saved["top_id"].reshape(copies, len(names), -1)[-1], saved["top_id"][few])
 
 
+@pytest.mark.parametrize("T", [2, 700])
+def test_logits_that_outgrow_the_first_base(cuda_lib, T):
+    """Scaled logits beyond 2^20, from the start or only later, both signs: the sums change their form on the way."""
+    V = 30000
+    i = torch.arange(V, dtype=torch.float64)
+    late = torch.cos(i)
+    late[-9:] = 5.0e6 + torch.arange(9).double()  # fp32 holds these
+    early = 3.0e6 - torch.floor(i / 3000)
+    below = -4.0e6 + (i % 7)
+    steps = torch.where(i > 20000, 1.2e6, torch.where(i > 9000, 6.0e5, 0.0)).double() + (i % 5)
+    rows = torch.stack([late, early, below, steps]).float()
+    z = rows.repeat(-(-T // 4) + 1, 1)[:max(T, 4)]
+    tau = torch.full((z.shape[0],), 0.75)
+    gen = torch.Generator().manual_seed(1)
+    tokens = torch.randint(V, (z.shape[0], 2), generator=gen)
+    tokens[:, 1] = V - 1
+    lp, saved = cuda_lib.sts_token_logprobs(z.cuda(), tokens.cuda(), temperature=tau.cuda(), top_n=6, entropy=True)
+    few = slice(0, 4)
+    _check_forward(z[few], tau[few], tokens[few], 6, lp[few], {k: v[few] for k, v in saved.items()}, V)
+    assert torch.equal(saved["entropy"][-4:].sort().values, saved["entropy"][few].sort().values) or z.shape[0] % 4
+    g = torch.ones(z.shape[0], 2, device="cuda")
+    dz = cuda_lib.sts_token_logprobs_backward(z.cuda(), tokens.cuda(), saved, g, temperature=tau.cuda())
+    assert torch.isfinite(dz).all() and dz.double().sum(1).abs().max() < 1e-3  # a gradient of log probabilities sums to 0
+
+
 def test_invalid_rows_do_not_touch_their_neighbours(cuda_lib):
     sts = cuda_lib
     V = 9000
