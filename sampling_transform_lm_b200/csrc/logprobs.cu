@@ -17,8 +17,9 @@
 //   x_i = c z_i - b,  c = log2(e) / tau,  S' = sum 2^x_i,  S'_1 = sum 2^x_i x_i
 // Any base gives the same quotients, so b is c times the maximum of the first
 // chunk of 2,048 to 8,192 elements and moves, a thread at a time, only when an
-// element exceeds it by more than a factor of 2 (a larger x would carry a larger
-// rounding into the terms that matter). An element costs a clamp, an FMA, an
+// element, or the bound of the alternatives (below), exceeds it by more than a
+// factor of 2 (a larger x would carry a larger rounding into the terms that
+// matter, and from 128 on 2^x is infinite). An element costs a clamp, an FMA, an
 // exponential and two sums; fp32 logits a second FMA, for what c's rounding
 // leaves (16-bit logits are themselves rounded by 2^-9 or 2^-11; there c's 2^-24
 // is a temperature half a step off, put right in log_sum by its derivative). The clamp keeps x at -200 or above (2^-200 is 0 in
@@ -560,6 +561,7 @@ __global__ void __launch_bounds__(kT, 1024 / kT) forward_kernel(const FwdArgs a)
     }
     const float vmax = largest(v);  // NaN where one is
     bool equal = false;  // whether ties with the bound still count
+    float raise = kNegInf;  // where this thread's base moves to
     if (!bound) {
       first_bound(sm, vmax, groups, n);
       if (sm.cut > kNegInf) {
@@ -567,8 +569,7 @@ __global__ void __launch_bounds__(kT, 1024 / kT) forward_kernel(const FwdArgs a)
         equal = true;  // the n elements of the bound are of this very chunk
         cut = sm.cut;
         // the base: the chunk's maximum
-        const float to = fmaxf(fminf(sm.chunk_max, -kLowest), s.base);
-        rebase(s, to, c);
+        raise = fmaxf(fminf(sm.chunk_max, -kLowest), s.base);
       }
       __syncthreads();  // group_max, cut and chunk_max are free again
     } else if (it >= next_tighten && a.n > 1) {
@@ -582,9 +583,12 @@ __global__ void __launch_bounds__(kT, 1024 / kT) forward_kernel(const FwdArgs a)
         if (tid < n) sm.keys[tid] = sm.top[tid];
         if (tid == 0) sm.count = (uint32_t)n;
         cut = fmaxf(cut, key_logit(sm.top[n - 1]));
+        // what lies below the bound is not looked at, so no base stays behind it
+        if ((cut - s.base) * c.hi > 1.f && cut < INFINITY) raise = cut;
       }
       __syncthreads();
     }
+    if (raise > kNegInf) rebase(s, raise, c);
     // Something above the bound (or at it while ties count; without one, above
     // -inf), or a NaN: the warp looks at the thread's elements together, a lane each, in the
     // buffer (rare: about n elements for each doubling of the row). The thread

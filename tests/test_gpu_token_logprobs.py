@@ -446,3 +446,108 @@ def test_no_rows(cuda_lib):
     lp, saved = cuda_lib.sts_token_logprobs(z, torch.empty(0, 2, dtype=torch.int64, device="cuda"), top_n=2)
     assert lp.shape == (0, 2) and saved["top_id"].shape == (0, 2)
     assert cuda_lib.sts_token_logprobs_backward(z, None, saved).shape == (0, 50)
+
+
+def _check_gradient(sts, z, tau, tokens, n, view, saved, ref, dtype, seed):
+    """The gradient from the same saved scalars, of logprobs, entropy and alternatives together."""
+    T, V = z.shape
+    gen = torch.Generator().manual_seed(seed)
+    g, h, gt = torch.randn(T, tokens.shape[1], generator=gen), torch.randn(T, generator=gen), torch.randn(T, n, generator=gen)
+    dz = sts.sts_token_logprobs_backward(view, tokens.cuda(), saved, g.cuda(), grad_entropy=h.cuda(), grad_top=gt.cuda(),
+                                         temperature=tau.cuda())
+    z64, tau64, h64 = z.double().numpy(), tau.double().numpy(), h.double().numpy()
+    want, tol = _grad_reference(z64, tau64, tokens.numpy(), n, g.double().numpy(), h64, gt.double().numpy(), ref)
+    tiny = {"fp32": 1e-37, "bf16": 1e-37, "fp16": 2.0 ** -24}[dtype]
+    # a probability below 2^-126 is flushed to 0 by the exponential, and with it p (G + h (ln p + entropy)) / tau:
+    # at tau = 0.01, ln p = -88, |h| = 3 that is 1.2e-38 * 100 * 264 = 3e-34, beyond what `tiny` holds
+    size = np.abs(g.double().numpy()).sum(1) + np.abs(gt.double().numpy()).sum(1)
+    lp = np.where(np.isfinite(ref["lp"]), np.abs(ref["lp"]), 0.0)
+    flush = 2.0 ** -126 * (size[:, None] + np.abs(h64)[:, None] * (lp + ref["entropy"][:, None])) / tau64[:, None]
+    err = np.abs(dz.double().cpu().numpy() - want)
+    lim = tol + HALF_STEP[dtype] * (np.abs(want) + tol) + tiny + np.where(ref["p"] < 2.0 ** -125, flush, 0.0)
+    bad = np.unravel_index((err / lim).argmax(), err.shape)
+    assert (err <= lim).all(), (err[bad], lim[bad], want[bad], ref["p"][bad], ref["lp"][bad])
+
+
+def _between_rows(V, chunk, n, gen):
+    """An ordinary first chunk, more than n logits near 500 in the next two, then logits near 400 and 300: far above
+    the first chunk, below the n-th largest. Rows differ in where the 400s start; the last has them only at the end."""
+    z = torch.randn(4, V, generator=gen)
+    for r in range(4):
+        high = chunk + torch.randperm(min(2 * chunk, V - chunk), generator=gen)[:n + 8]
+        z[r, high] = 500 + torch.randn(len(high), generator=gen)
+        start = min((3, 4, 5, 6)[r] * chunk, V - 600) if r < 3 else V - 600
+        at = start + torch.randperm(V - start, generator=gen)[:300]
+        z[r, at[:200]] = 400 + torch.randn(200, generator=gen)
+        z[r, at[200:]] = 300 + torch.randn(100, generator=gen)
+    return z
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("V,copies", [(50021, 150), (152064, 100), (262144, 1)])  # 128 and 256 threads, and clusters
+@pytest.mark.parametrize("n", [2, 8, 20, 64])
+def test_logits_between_the_first_chunk_and_the_bound(cuda_lib, dtype, V, copies, n):
+    """The bound of the alternatives rises over what the first chunk held; logits between the two enter the sums of
+    threads that never met one above the bound."""
+    gen = torch.Generator().manual_seed(V + n)
+    threads = 128 if V <= 65536 else 256
+    z = _between_rows(V, threads * 4 * (4 if dtype == "fp32" else 8), n, gen).to(DTYPES[dtype])
+    tau = torch.tensor([1.0, 0.7, 1.3, 1.0])
+    tokens = torch.randint(V, (4, 2), generator=gen)
+    tokens[:, 1] = z.argmax(1)
+    view = z.cuda().repeat(copies, 1)
+    lp, saved = cuda_lib.sts_token_logprobs(view, tokens.cuda().repeat(copies, 1), temperature=tau.cuda().repeat(copies), top_n=n,
+                                            entropy=True)
+    assert (saved["flags"] == 0).all()
+    few = {k: v[-4:].contiguous() for k, v in saved.items()}
+    ref = _check_forward(z, tau, tokens, n, lp[-4:], few, V)
+    for k, v in saved.items():
+        assert torch.equal(v.reshape(copies, 4, -1), v[-4:].reshape(1, 4, -1).expand(copies, 4, -1)), k
+    _check_gradient(cuda_lib, z, tau, tokens, n, view[-4:], few, ref, dtype, n)
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("T,V", [(3, 262144), (300, 152064), (300, 60000)])
+@pytest.mark.parametrize("mask", [-100.0, -1000.0])
+@pytest.mark.parametrize("n", [2, 5, 20])
+def test_a_finite_mask_that_is_added(cuda_lib, dtype, T, V, mask, n):
+    """400 allowed tokens, none in the first part of the vocabulary; what is not allowed is lowered, not removed."""
+    gen = torch.Generator().manual_seed(V + n)
+    rows = 4
+    z = torch.randn(rows, V, generator=gen) * 2 + mask
+    for r in range(rows):
+        allowed = 10000 + torch.randperm(V - 10000, generator=gen)[:400]
+        z[r, allowed] -= mask
+    z = z.to(DTYPES[dtype])
+    tau = torch.ones(rows)
+    tokens = torch.randint(V, (rows, 2), generator=gen)
+    tokens[:, 1] = z.argmax(1)
+    pick = torch.arange(T) % rows
+    view = z.cuda()[pick.cuda()]
+    lp, saved = cuda_lib.sts_token_logprobs(view, tokens.cuda()[pick.cuda()], top_n=n, entropy=True)
+    rows = min(rows, T)
+    few = {k: v[:rows].contiguous() for k, v in saved.items()}
+    ref = _check_forward(z[:rows], tau[:rows], tokens[:rows], n, lp[:rows], few, V)
+    _check_gradient(cuda_lib, z[:rows], tau[:rows], tokens[:rows], n, view[:rows], few, ref, dtype, n)
+
+
+@pytest.mark.parametrize("dtype,V", [("bf16", 152064), ("fp32", 152064), ("fp16", 50021)])
+@pytest.mark.parametrize("temperature", [0.01, 0.02, 0.05])
+@pytest.mark.parametrize("n", [2, 5, 64])
+def test_low_temperatures_over_a_whole_vocabulary(cuda_lib, dtype, V, temperature, n):
+    """Logits as a model gives them (a few hot tokens), a block a row; 32 of the rows against the definition."""
+    gen = torch.Generator().manual_seed(n)
+    T, few = 640, 32
+    z = torch.randn(few, V, generator=gen) * 2
+    hot = torch.randint(V, (few, 40), generator=gen)
+    z.scatter_add_(1, hot, 4 + 8 * torch.rand(few, 40, generator=gen))
+    z = z.to(DTYPES[dtype])
+    tau = torch.full((few,), temperature)
+    tokens = hot[:, :2].contiguous()
+    view = z.cuda().repeat(T // few, 1)
+    lp, saved = cuda_lib.sts_token_logprobs(view, tokens.cuda().repeat(T // few, 1), temperature=tau.cuda().repeat(T // few), top_n=n,
+                                            entropy=True)
+    assert torch.isfinite(saved["lse"]).all() and torch.isfinite(saved["entropy"]).all()
+    part = {k: v[-few:].contiguous() for k, v in saved.items()}
+    ref = _check_forward(z, tau, tokens, n, lp[-few:], part, V)
+    _check_gradient(cuda_lib, z, tau, tokens, n, view[-few:], part, ref, dtype, n)
