@@ -409,13 +409,18 @@ typedef struct {
  * transposed hidden states as B give dW. C's rows are ldc elements apart. It
  * must not overlap A, B or the scales. M = 0 and N = 0 are allowed. One kernel
  * launch, no scratch memory: ws may be NULL, or 256 bytes for the status word
- * that sts_get_status reads (STS_ERR_TIMEOUT); without it a device-side wait
- * that gave up is not reported. The result depends on the shapes and the
+ * that sts_get_status reads (STS_ERR_TIMEOUT). With or without it, what a
+ * device-side wait that gave up leaves unknown of C is NaN. The result depends on the shapes and the
  * device's SM count, not on what else runs. */
 sts_status sts_block_scaled_product(const sts_block_operand* A, const sts_block_operand* B,
                                     int64_t K, const float* temperature, void* C, int c_dtype,
                                     int64_t ldc, int accumulate, void* ws, size_t ws_bytes,
                                     sts_stream_t stream);
+
+/* Test hook: until it is called again, thread block `block` of every
+ * sts_block_scaled_product of this process does nothing, as if its first wait
+ * had given up; -1 (the initial state): none does. */
+void sts_probe_product_timeout(int64_t block);
 
 /* Rows of logits and the tokens that are asked of them. */
 typedef struct {

@@ -119,6 +119,7 @@ EXPORTED_SYMBOLS = (
     "sts_tp_finish",
     "sts_block_quantize",
     "sts_block_scaled_product",
+    "sts_probe_product_timeout",
     "sts_token_logprobs",
     "sts_token_logprobs_backward",
 )
@@ -259,6 +260,8 @@ def load():
                                              ctypes.POINTER(_BlockOperand), I64, P, P, I, I64, I, P,
                                              S, P]
     lib.sts_block_scaled_product.restype = ctypes.c_int
+    lib.sts_probe_product_timeout.argtypes = [I64]
+    lib.sts_probe_product_timeout.restype = None
     lib.sts_token_logprobs.argtypes = [ctypes.POINTER(_TokenRows), P, ctypes.POINTER(_TokenStats), P]
     lib.sts_token_logprobs.restype = ctypes.c_int
     lib.sts_token_logprobs_backward.argtypes = [ctypes.POINTER(_TokenRows),
@@ -922,8 +925,9 @@ def sts_block_scaled_product(A, a_scale, B, b_scale, *, temperature=None, out=No
 
     Each block of 128 is summed on the tensor cores and scaled in fp32. The rows are multiplied by
     1 / ``temperature`` [M] where it is given (the scaled logits of an 8-bit head). C is ``out`` or new,
-    fp32 (default) or bf16; with ``accumulate`` the product is added to ``out`` (fp32). With
-    ``check`` the call synchronises and raises if a device-side wait gave up."""
+    fp32 (default) or bf16; with ``accumulate`` the product is added to ``out`` (fp32). What a
+    device-side wait that gave up leaves unknown is NaN; with ``check`` the call synchronises and
+    raises on it."""
     lib = load()
     a = _block_operand(A, a_scale, "A", True)
     b = _block_operand(B, b_scale, "B", False)

@@ -43,6 +43,7 @@
 // memory and handing blocks over 0.34, the FMAs 0.12 more, the writing of C 10 %.
 // Sixteen warps of sums (96 registers), 32 columns a read (spills) and waiting by
 // polling were each slower by 1 to 20 %.
+#include <atomic>
 #include <cstring>
 
 #include <cooperative_groups.h>
@@ -82,7 +83,7 @@ struct Shape {
   static constexpr uint32_t kSlot = kBlockScales * kGroupBlocks * 4;
   static constexpr uint32_t kStagingBytes = kWide ? kSumWarps * 2 * kStaging : 0;
   static constexpr int kBars = 2 * kStages + 2 * kSlots + 2 * kBufs + 1;
-  static constexpr size_t kSmem = (size_t)kStages * kStage + kStagingBytes + kSlots * kSlot + kBars * 8 + 16;
+  static constexpr size_t kSmem = (size_t)kStages * kStage + kStagingBytes + kSlots * kSlot + kBars * 8 + 8 + kSumWarps * 4;
   // a split's sums: a line for each m of C (wide: a lane, narrow: a column), n
   // along it; 16 bytes more a line, against bank conflicts
   static constexpr int kLines = kWide ? kLanes : NT, kLong = kWide ? NT : kLanes;
@@ -108,6 +109,7 @@ struct ProductArgs {
   int accumulate;
   int split;            // CTAs per tile (cluster size)
   int tma_out;          // C can be written by TMA (wide)
+  int give_up;          // a block that acts as if its first wait had given up, or -1
   int* err;
 };
 
@@ -298,6 +300,16 @@ __device__ __forceinline__ void finish(const ProductArgs& p, int m, int n, float
   put(c, v);
 }
 
+// NaN over rows x cols (0 or fewer: nothing) of C, by one warp.
+template <typename O>
+__device__ __forceinline__ void blank(O* c, int64_t ldc, int rows, int cols) {
+#pragma unroll 1
+  for (int m = 0; m < rows; ++m)
+#pragma unroll 1
+    for (int n = (int)threadIdx.x & 31; n < cols; n += 32)
+      put(c + m * ldc + n, __int_as_float(0x7fc00000));
+}
+
 // 1 / tau_m, by which row m's sums are multiplied: a division an element would
 // take longer than the multiplication of two blocks, and round once less.
 __device__ __forceinline__ float over_tau(const ProductArgs& p, int m) {
@@ -346,6 +358,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* drain = tempty + kBufs;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+  int* stopped = reinterpret_cast<int*>(tmem_holder + 2);  // the tile at which a warp of sums gave up
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -372,8 +385,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(smem_u32(drain), 1);
     // the ring's swizzle needs 1,024-byte stages; without them nothing runs
-    *abort_flag = (smem_u32(smem) & 1023u) != 0 ? 1 : 0;
-    if (*abort_flag && p.err) atomicCAS(p.err, 0, (int)STS_ERR_OVERFLOW);
+    const int bad = (smem_u32(smem) & 1023u) != 0        ? (int)STS_ERR_OVERFLOW
+                    : (int)blockIdx.x == p.give_up ? (int)STS_ERR_TIMEOUT
+                                                   : 0;
+    *abort_flag = bad != 0 ? 1 : 0;
+    for (int w = 0; w < kSumWarps; ++w) stopped[w] = bad != 0 ? tile0 : tiles;
+    if (bad != 0 && p.err) atomicCAS(p.err, 0, bad);
     fence_barrier_init();
     fence_proxy_async_smem();
   }
@@ -394,8 +411,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const int quarter = warp & 3;
   const int half = warp >= 8 ? 1 : 0;
-  int last_l = 0, last_c = 0;
-  bool have = false;
 
   // Warps 0 and 1 have 512 clocks (wide) for a block: their loops go through one
   // turn of the rings at a time, so that barriers, addresses and phases are
@@ -484,6 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             fphase ^= 1u;
           }
         }
+        if (!ok) break;  // a group that is not whole is not handed over
         commit(mine, smem_u32(&tfull[b]));
         kb += n;
         if (kb == kb1) kb = kb0;
@@ -691,11 +707,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      if (!ok) break;
+      if (!ok) {
+        if (lane == 0) stopped[warp - 4] = t;
+        break;
+      }
       if (p.split > 1) {
-        last_l = tl;
-        last_c = tc;
-        have = true;
+        // one tile a cluster: its sums are joined below
       } else if constexpr (!kWide) {
         const int row = quarter * 32 + lane;
         const int n = tl * p.height + row;
@@ -777,7 +794,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (kWide && lane == 0) bulk_wait_all();
     __syncwarp();
-    if (have) {
+    if (p.split > 1) {
       // One tile per cluster. Every stage has been read by now (the sums wait
       // for the last MMA), so the ring holds the sums, a line for each m.
       float* sums = reinterpret_cast<float*>(smem);
@@ -802,7 +819,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       float* sums = reinterpret_cast<float*>(smem);
       cg::cluster_group cluster = cg::this_cluster();
       cluster.sync();
-      if (have) {
+      {
+        int last_l, last_c;
+        tile_coords<kWide>(p, tile0, last_l, last_c);
         // the CTAs divide the lines; the parts are added in the order of k
         for (int j = part + p.split * (warp - 4); j < S::kLines; j += p.split * kSumWarps) {
           const int m = (kWide ? last_l * kLanes : last_c * NT) + j;
@@ -840,6 +859,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 
   __syncthreads();
+  if (*abort_flag != 0 && warp >= 4) {
+    // After a wait that gave up, this warp's share of the tile that it was at and
+    // of those to come is unknown; of a split, the whole tile, which by now every
+    // other part has written.
+    for (int t = p.split > 1 ? tile0 : stopped[warp - 4]; t < tiles; t += step) {
+      int tl, tc;
+      tile_coords<kWide>(p, t, tl, tc);
+      const int l0 = tl * p.height + quarter * 32, l = min(32, p.height - quarter * 32);
+      const int c0 = tc * NT + half * kHalf;
+      const int m0 = kWide ? l0 : c0, n0 = kWide ? c0 : l0;
+      blank(static_cast<O*>(p.C) + (int64_t)m0 * p.ldc + n0, p.ldc, min(kWide ? l : kHalf, p.M - m0),
+            min(kWide ? kHalf : l, p.N - n0));
+    }
+  }
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem_base, S::kTmemCols);
@@ -890,6 +923,8 @@ cudaError_t launch_out(int NT, bool uniform, const Maps& maps, const ProductArgs
 
 constexpr int64_t kMost = (int64_t(1) << 31) - 1024;
 
+std::atomic<int64_t> g_give_up{-1};  // sts_probe_product_timeout
+
 // Which form. Above 128 rows of A the wide one, up to 64 the narrow one; between
 // them by the rounds of tiles that each takes over the SMs. A round of the wide
 // form's tiles takes about as long as its blocks along k and 12 more (its results
@@ -928,6 +963,10 @@ sts_status check_operand(const sts_block_operand* o, int64_t K, bool rows_only) 
 }  // namespace sts
 
 using namespace sts;
+
+extern "C" void sts_probe_product_timeout(int64_t block) {
+  g_give_up.store(block >= 0 && block <= kMost ? block : -1, std::memory_order_relaxed);
+}
 
 extern "C" sts_status sts_block_scaled_product(const sts_block_operand* A,
                                                const sts_block_operand* B, int64_t K,
@@ -988,6 +1027,7 @@ extern "C" sts_status sts_block_scaled_product(const sts_block_operand* A,
   p.C = C;
   p.ldc = ldc;
   p.accumulate = accumulate ? 1 : 0;
+  p.give_up = (int)g_give_up.load(std::memory_order_relaxed);
   const int64_t tiles = tiles_l * tiles_c;
   // a stretch of k for each of 2, 4 or 8 CTAs while the SMs are not full, none
   // below 4 blocks (300 x 2,048 x 8,192: 25 us, whole 39; 1 x 512 x 16,384: 16, 31)

@@ -260,6 +260,42 @@ def test_product_not_finite(cuda_lib):
     assert torch.equal(torch.isnan(C), nan)
 
 
+@pytest.mark.parametrize("M,N,K,b_rows,out,block", [
+    (5, 30000, 300, 128, "fp32", 3),  # narrow: two tiles of the block's are lost
+    (100, 30001, 200, 1, "bf16", 147),
+    (1000, 20000, 300, 128, "fp32", 0),  # wide, by TMA
+    (1000, 20003, 300, 128, "fp32", 7),  # wide, rows that TMA cannot address
+    (700, 20000, 130, 1, "bf16", 11),
+    (40, 300, 9000, 128, "fp32", 1),  # a part of a split over k: the whole tile depends on it
+    (300, 400, 9000, 1, "fp32", 8),
+    (300, 400, 9000, 128, "bf16", 7)])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_a_product_that_gives_up_does_not_pass_for_one(cuda_lib, M, N, K, b_rows, out, block, accumulate):
+    """A block that gives up leaves NaN where its results belong, nothing else changes, and the status says so."""
+    if accumulate and out != "fp32":
+        accumulate = False
+    gen = torch.Generator().manual_seed(12)
+    A, sa = _operand(gen, M, K, E4M3, 1)
+    B, sb = _operand(gen, N, K, E4M3, b_rows)
+    plain = cuda_lib.sts_block_scaled_product(A, sa, B, sb, out=torch.full((M, N), 7.0, dtype=SRC[out], device="cuda"),
+                                              accumulate=accumulate, check=True)
+    C = torch.full((M, N), 7.0, dtype=SRC[out], device="cuda")
+    probe = cuda_lib.load().sts_probe_product_timeout
+    probe(block)
+    try:
+        cuda_lib.sts_block_scaled_product(A, sa, B, sb, out=C, accumulate=accumulate)
+        with pytest.raises(cuda_lib.StsError) as e:
+            cuda_lib.sts_block_scaled_product(A, sa, B, sb, check=True)
+        assert e.value.status == 11
+    finally:
+        probe(-1)
+    lost = torch.isnan(C)
+    assert lost.any() and not lost.all()
+    assert torch.equal(C[~lost], plain[~lost])
+    again = cuda_lib.sts_block_scaled_product(A, sa, B, sb, out=torch.full_like(C, 7.0), accumulate=accumulate, check=True)
+    assert torch.equal(again, plain)
+
+
 def test_product_empty(cuda_lib):
     gen = torch.Generator().manual_seed(4)
     A, sa = _operand(gen, 4, 64, E4M3, 1)
