@@ -371,9 +371,10 @@ typedef enum {
  *   q     = x (1 / scale) (reciprocal and product rounded to fp32; x / scale
  *           where scale < 2^-126), limited to +-top, rounded to nearest even;
  *           NaN where x is not finite
- * x_dtype: STS_DTYPE_F32, _BF16 or _F16; element (r, k) at x[r * stride_r + k *
- * stride_k], one of the strides 1 (a transposed view has stride_r == 1), the
- * other at least the extent it steps over. q_dtype: STS_DTYPE_E4M3 or _E5M2;
+ * x_dtype: STS_DTYPE_F32, _BF16 or _F16, element-aligned (and scale to 4 bytes:
+ * else STS_ERR_SHAPE); element (r, k) at x[r * stride_r + k * stride_k], one of
+ * the strides 1 (a transposed view has stride_r == 1), the other at least the
+ * extent it steps over. q_dtype: STS_DTYPE_E4M3 or _E5M2;
  * q's rows are q_ld >= K bytes apart (sts_block_scaled_product wants a
  * multiple of 16), bytes past K are left as they are. scale [ceil(R /
  * block_rows)][scale_ld >= ceil(K / 128)]. R = 0 is allowed (nothing is

@@ -485,6 +485,9 @@ extern "C" sts_status sts_block_quantize(int64_t R, int64_t K, const void* x, in
   if (q_ld < K || scale_ld < k_blocks) return STS_ERR_SHAPE;
   if (R == 0) return STS_OK;
   if (!x || !q || !scale) return STS_ERR_NULL;
+  const unsigned es = x_dtype == STS_DTYPE_F32 ? 4 : 2;
+  if (reinterpret_cast<uintptr_t>(x) % es != 0 || (reinterpret_cast<uintptr_t>(scale) & 3u) != 0)
+    return STS_ERR_SHAPE;
   QuantArgs a{};
   a.x = x;
   a.R = R;

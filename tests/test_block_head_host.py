@@ -34,6 +34,12 @@ def test_quantize_refusals(lib, change, status):
     assert _quantize(lib, **change) == status
 
 
+@pytest.mark.parametrize("change", [dict(x=P + 1), dict(x=P + 2, xt=F32), dict(x=P + 1, xt=F16), dict(scale=P + 1), dict(scale=P + 2),
+                                    dict(x=P + 1, sr=1, sk=4), dict(x=P + 3, br=128)])
+def test_quantize_refuses_what_is_not_aligned(lib, change):
+    assert _quantize(lib, **change) == SHAPE
+
+
 def _operand(rows=40, q=P, dtype=E4M3, ld=256, scale=P, sr=2, sk=1, block_rows=1):
     return _BlockOperand(q, dtype, rows, ld, scale, sr, sk, block_rows)
 
