@@ -377,7 +377,8 @@ typedef enum {
  * extent it steps over. q_dtype: STS_DTYPE_E4M3 or _E5M2;
  * q's rows are q_ld >= K bytes apart (sts_block_scaled_product wants a
  * multiple of 16), bytes past K are left as they are. scale [ceil(R /
- * block_rows)][scale_ld >= ceil(K / 128)]. R = 0 is allowed (nothing is
+ * block_rows)][scale_ld >= ceil(K / 128)]. x, q and scale may lie between one
+ * another's rows, but share no byte (STS_ERR_SHAPE). R = 0 is allowed (nothing is
  * written). Asynchronous, allocates nothing, one kernel launch.
  * STS_ERR_DTYPE, STS_ERR_SHAPE, STS_ERR_NULL. */
 sts_status sts_block_quantize(int64_t R, int64_t K, const void* x, int x_dtype, int64_t stride_r,

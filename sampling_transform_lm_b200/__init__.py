@@ -854,7 +854,8 @@ def sts_block_quantize(x, *, block_rows=1, dtype=_E4M3, q=None, scale=None, stre
 
     Returns ``(q [R, K], scale [ceil(R / block_rows), ceil(K / 128)])`` with x ~ q * scale.
     ``q``'s rows are a multiple of 16 bytes apart, as ``sts_block_scaled_product`` wants them
-    (a view where K is no multiple of 16). ``q`` and ``scale`` may be given to be written."""
+    (a view where K is no multiple of 16). ``q`` and ``scale`` may be given to be written; they
+    share no memory with ``x`` or each other."""
     lib = load()
     if dtype not in (_E4M3, _E5M2):
         raise StsError(STS_ERR_DTYPE, f"dtype must be an 8-bit float, got {dtype}")

@@ -461,6 +461,38 @@ cudaError_t launch_t(const QuantArgs& a, bool e5, bool transposed, int block_row
             : launch<T, false, false>(a, transposed, block_rows, st);
 }
 
+// Rows of bytes in memory, at least their width apart.
+struct Rows {
+  uintptr_t at;
+  int64_t n;
+  uintptr_t pitch, width;
+  uintptr_t end() const { return at + (uintptr_t)(n - 1) * pitch + width; }
+};
+
+// Whether a row of one meets a row of the other. Rows of one pitch, side by side
+// (codes and their scales in one record), and rows that lie apart are told at once.
+bool meet(Rows a, Rows b) {
+  if (a.n < 1 || b.n < 1 || a.end() <= b.at || b.end() <= a.at) return false;
+  if (a.n > 1 && b.n > 1 && a.pitch == b.pitch) {
+    const uintptr_t p = a.pitch, d = b.at >= a.at ? (b.at - a.at) % p : (p - (a.at - b.at) % p) % p;
+    if (d >= a.width && d + b.width <= p) return false;
+  }
+  if (b.n < a.n) {
+    const Rows c = a;
+    a = b;
+    b = c;
+  }
+  for (int64_t i = 0; i < a.n; ++i) {
+    const uintptr_t from = a.at + (uintptr_t)i * a.pitch, to = from + a.width;
+    if (to <= b.at) continue;
+    // the last of b's rows that starts before this one ends
+    const uintptr_t j = b.n > 1 ? (to - 1 - b.at) / b.pitch : 0;
+    const uintptr_t last = j < (uintptr_t)b.n ? j : (uintptr_t)b.n - 1;
+    if (b.at + last * b.pitch + b.width > from) return true;
+  }
+  return false;
+}
+
 }  // namespace
 }  // namespace sts
 
@@ -488,6 +520,14 @@ extern "C" sts_status sts_block_quantize(int64_t R, int64_t K, const void* x, in
   const unsigned es = x_dtype == STS_DTYPE_F32 ? 4 : 2;
   if (reinterpret_cast<uintptr_t>(x) % es != 0 || (reinterpret_cast<uintptr_t>(scale) & 3u) != 0)
     return STS_ERR_SHAPE;
+  // blocks are written while others are still to be read
+  const int64_t scale_rows = block_rows == 1 ? R : (R + kBlock - 1) / kBlock;
+  const Rows in{reinterpret_cast<uintptr_t>(x), transposed ? K : R, (uintptr_t)ld * es,
+                (uintptr_t)(transposed ? R : K) * es};
+  const Rows codes{reinterpret_cast<uintptr_t>(q), R, (uintptr_t)q_ld, (uintptr_t)K};
+  const Rows scales{reinterpret_cast<uintptr_t>(scale), scale_rows, (uintptr_t)scale_ld * 4,
+                    (uintptr_t)k_blocks * 4};
+  if (meet(in, codes) || meet(in, scales) || meet(codes, scales)) return STS_ERR_SHAPE;
   QuantArgs a{};
   a.x = x;
   a.R = R;

@@ -34,10 +34,61 @@ def test_quantize_refusals(lib, change, status):
     assert _quantize(lib, **change) == status
 
 
-@pytest.mark.parametrize("change", [dict(x=P + 1), dict(x=P + 2, xt=F32), dict(x=P + 1, xt=F16), dict(scale=P + 1), dict(scale=P + 2),
+@pytest.mark.parametrize("change", [dict(x=P + 1), dict(x=P + 2, xt=F32), dict(x=P + 1, xt=F16), dict(scale=(1 << 42) + 1), dict(scale=(1 << 42) + 2),
                                     dict(x=P + 1, sr=1, sk=4), dict(x=P + 3, br=128)])
 def test_quantize_refuses_what_is_not_aligned(lib, change):
-    assert _quantize(lib, **change) == SHAPE
+    assert _quantize(lib, **dict(dict(q=1 << 41, scale=1 << 42), **change)) == SHAPE
+
+
+def _bytes(at, n, pitch, width):
+    return {b for i in range(n) for b in range(at + i * pitch, at + i * pitch + width)}
+
+
+def _share(R, K, x, es, ld, transposed, q, q_ld, scale, s_ld, br):
+    a = _bytes(x, K if transposed else R, ld * es, (R if transposed else K) * es)
+    b = _bytes(q, R, q_ld, K)
+    c = _bytes(scale, -(-R // br), s_ld * 4, -(-K // 128) * 4)
+    return bool(a & b or a & c or b & c)
+
+
+@pytest.mark.parametrize("change,status", [
+    (dict(q=P, scale=1 << 40), SHAPE),  # in place
+    (dict(q=P + 4 * 512 - 1, scale=1 << 40), SHAPE),  # x's last byte
+    (dict(q=1 << 40, scale=P), SHAPE), (dict(q=1 << 40, scale=(1 << 40) + 252), SHAPE),
+    (dict(sr=512, q=P + 512, q_ld=1024, scale=P + 768, s_ld=256), None),  # a record a row: source, codes, scales
+    (dict(sr=512, q=P + 511, q_ld=1024, scale=P + 768, s_ld=256), SHAPE),
+    (dict(sr=512, q=P + 512, q_ld=1024, scale=P + 764, s_ld=256), SHAPE),
+    (dict(sr=512, q=P - 256, q_ld=1024, scale=P + 512, s_ld=256), None),
+    (dict(sr=512, q=P - 255, q_ld=1024, scale=1 << 40), SHAPE),
+    (dict(sr=512, q=P + 512, q_ld=512, scale=1 << 40), SHAPE),  # other pitches: the second row's codes meet x's second row
+    (dict(sr=512, q=P + 512, q_ld=2048, scale=1 << 40), None)])
+def test_quantize_refuses_results_inside_the_source_or_each_other(lib, change, status):
+    args = dict(dict(q_ld=256, s_ld=2, sr=256), **change)
+    shares = _share(4, 256, P, 2, args["sr"], False, args["q"], args["q_ld"], args["scale"], args["s_ld"], 1)
+    assert shares == (status == SHAPE)
+    got = _quantize(lib, **change)
+    assert (got == SHAPE) == shares and (shares or got not in (OK, NULL, DTYPE))
+
+
+def test_quantize_tells_overlap_byte_by_byte(lib):
+    """Any small layout is refused exactly when a byte is shared."""
+    import random
+
+    rng = random.Random(0)
+    told = [0, 0]
+    for _ in range(3000):
+        R, K = rng.randint(1, 5), rng.randint(1, 20)
+        br, tr = rng.choice([1, 128]), rng.random() < 0.4
+        ld = rng.randint(R if tr else K, 40)
+        q_ld, s_ld = rng.randint(K, 90), rng.randint(1, 22)
+        x, q, scale = P, P + rng.randint(-80, 300), P + 4 * rng.randint(-30, 120)
+        if tr and ld == 1:
+            continue
+        got = _quantize(lib, R=R, K=K, x=x, sr=1 if tr else ld, sk=ld if tr else 1, br=br, q=q, q_ld=q_ld, scale=scale, s_ld=s_ld)
+        shares = _share(R, K, x, 2, ld, tr, q, q_ld, scale, s_ld, br)
+        assert (got == SHAPE) == shares, (R, K, br, tr, ld, q_ld, s_ld, q - P, scale - P)
+        told[shares] += 1
+    assert min(told) > 300
 
 
 def _operand(rows=40, q=P, dtype=E4M3, ld=256, scale=P, sr=2, sk=1, block_rows=1):
