@@ -424,7 +424,8 @@ sts_status sts_block_scaled_product(const sts_block_operand* A, const sts_block_
  * had given up; -1 (the initial state): none does. */
 void sts_probe_product_timeout(int64_t block);
 
-/* Rows of logits and the tokens that are asked of them. */
+/* Rows of logits and the tokens that are asked of them. Every array here and
+ * below is aligned to its elements (STS_ERR_SHAPE). */
 typedef struct {
   const void* logits;       /* [T][ld], the first V of each row, element-aligned */
   int dtype;                /* STS_DTYPE_F32, _BF16 or _F16 */

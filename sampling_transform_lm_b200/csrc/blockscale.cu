@@ -985,7 +985,8 @@ extern "C" sts_status sts_block_scaled_product(const sts_block_operand* A,
     return STS_ERR_WORKSPACE;
   if (A->rows == 0 || B->rows == 0) return STS_OK;
   if (!C) return STS_ERR_NULL;
-  if ((reinterpret_cast<uintptr_t>(C) % (c_dtype == STS_DTYPE_F32 ? 4u : 2u)) != 0)
+  if ((reinterpret_cast<uintptr_t>(C) % (c_dtype == STS_DTYPE_F32 ? 4u : 2u)) != 0 ||
+      (reinterpret_cast<uintptr_t>(temperature) & 3u) != 0)
     return STS_ERR_SHAPE;
   int sms = 0;
   s = current_device(&sms);

@@ -1134,6 +1134,10 @@ cudaError_t launch_forward(const FwdArgs& a, int threads, cudaStream_t st) {
 
 constexpr int64_t kMost = (int64_t(1) << 31) - 1;
 
+bool aligned(const void* p, int bytes) {
+  return reinterpret_cast<uintptr_t>(p) % (unsigned)bytes == 0;
+}
+
 // Host checks shared by both directions; *done where there is nothing to do.
 sts_status check_token_rows(const sts_token_rows* r, bool* done) {
   *done = false;
@@ -1148,8 +1152,15 @@ sts_status check_token_rows(const sts_token_rows* r, bool* done) {
     return STS_OK;
   }
   if (!r->logits || (r->m > 0 && !r->tokens)) return STS_ERR_NULL;
-  if ((reinterpret_cast<uintptr_t>(r->logits) % (unsigned)es) != 0) return STS_ERR_SHAPE;
+  if (!aligned(r->logits, es) || (r->m > 0 && !aligned(r->tokens, 8)) || !aligned(r->temperature, 4))
+    return STS_ERR_SHAPE;
   return STS_OK;
+}
+
+bool aligned_stats(const sts_token_stats* s) {
+  return aligned(s->logit_max, 4) && aligned(s->log_sum, 4) && aligned(s->lse, 4) &&
+         aligned(s->entropy, 4) && aligned(s->flags, 4) && aligned(s->top_id, 8) &&
+         aligned(s->top_logprob, 4);
 }
 
 }  // namespace
@@ -1164,6 +1175,7 @@ extern "C" sts_status sts_token_logprobs(const sts_token_rows* rows, float* logp
   if (cs != STS_OK || done) return cs;
   if (!stats || (rows->m > 0 && !logprob)) return STS_ERR_NULL;
   if (rows->top_n > 0 && (!stats->top_id || !stats->top_logprob)) return STS_ERR_NULL;
+  if (!aligned_stats(stats) || !aligned(logprob, 4)) return STS_ERR_SHAPE;
   int sms = 0;
   const sts_status ds = current_device(&sms);
   if (ds != STS_OK) return ds;
@@ -1227,7 +1239,9 @@ extern "C" sts_status sts_token_logprobs_backward(const sts_token_rows* rows,
     return STS_ERR_NULL;
   if (grad_entropy && !saved->entropy) return STS_ERR_NULL;
   if (grad_top && rows->top_n > 0 && !saved->top_id) return STS_ERR_NULL;
-  if ((reinterpret_cast<uintptr_t>(dlogits) % (unsigned)os) != 0) return STS_ERR_SHAPE;
+  if (!aligned(dlogits, os) || !aligned_stats(saved) || !aligned(grad_logprob, 4) ||
+      !aligned(grad_entropy, 4) || !aligned(grad_top, 4))
+    return STS_ERR_SHAPE;
   // the gradient may take the logits' own place, and no other part of them
   const int es = elem_size(rows->dtype);
   const uintptr_t z0 = reinterpret_cast<uintptr_t>(rows->logits);

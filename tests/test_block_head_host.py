@@ -161,6 +161,31 @@ def test_backward_refusals(lib, change, status):
     assert _backward(lib, **change) == status
 
 
+@pytest.mark.parametrize("name,off", [("logit_max", 2), ("log_sum", 1), ("lse", 3), ("entropy", 2), ("flags", 2), ("top_id", 4),
+                                      ("top_logprob", 1)])
+def test_misaligned_statistics_are_refused(lib, name, off):
+    far = dict(out=1 << 40)
+    r, s = _rows(), _TokenStats(**dict(STATS, **{name: P + off}))
+    assert lib.sts_token_logprobs(ctypes.byref(r), P, ctypes.byref(s), None) == SHAPE
+    assert _backward(lib, stats={name: P + off}, **far) == SHAPE
+
+
+@pytest.mark.parametrize("change", [dict(rows=dict(tokens=P + 4)), dict(rows=dict(temperature=P + 2)), dict(g=P + 2), dict(h=P + 1),
+                                    dict(gt=P + 3)])
+def test_misaligned_rows_and_gradients_are_refused(lib, change):
+    assert _backward(lib, **change) == SHAPE
+    if "rows" in change:
+        r, s = _rows(**change["rows"]), _TokenStats(**STATS)
+        assert lib.sts_token_logprobs(ctypes.byref(r), P, ctypes.byref(s), None) == SHAPE
+    r, s = _rows(), _TokenStats(**STATS)
+    assert lib.sts_token_logprobs(ctypes.byref(r), P + 2, ctypes.byref(s), None) == SHAPE
+
+
+def test_a_misaligned_temperature_of_the_product_is_refused(lib):
+    A, B = _operand(), _operand()
+    assert lib.sts_block_scaled_product(ctypes.byref(A), ctypes.byref(B), 256, P + 2, P, F32, 40, 0, None, 0, None) == SHAPE
+
+
 def test_binding_refusals():
     bf = torch.zeros(4, 256, dtype=torch.bfloat16)
     with pytest.raises(sts.StsError) as e:
