@@ -924,8 +924,11 @@ struct RowCoef {
 };
 
 __device__ __forceinline__ float grad_of(float z, const RowCoef& k) {
-  const float d = fmaxf(z - k.zmax, kLowest);  // -inf - zmax: no 0 * inf below
-  const float x = fmaxf(fmaf(d, k.c, fmaf(d, k.lo, -k.l2s)), -200.f);
+  // c d comes first: where it leaves fp32 (masked tokens, low temperatures) x is
+  // -inf whatever lo d is, or NaN, which fmaxf drops. Added to lo d, which may be
+  // +inf, the exact product of the FMA would not count.
+  const float d = z - k.zmax;
+  const float x = fmaxf(fmaf(d, k.lo, fmaf(d, k.c, -k.l2s)), -200.f);
   return ex2(x) * fmaf(k.b, x, k.a);
 }
 

@@ -551,3 +551,29 @@ def test_low_temperatures_over_a_whole_vocabulary(cuda_lib, dtype, V, temperatur
     part = {k: v[-few:].contiguous() for k, v in saved.items()}
     ref = _check_forward(z, tau, tokens, n, lp[-few:], part, V)
     _check_gradient(cuda_lib, z, tau, tokens, n, view[-few:], part, ref, dtype, n)
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("mask", ["inf", "lowest"])
+def test_gradients_of_masked_tokens_at_low_temperatures(cuda_lib, dtype, mask):
+    """A masked token has a gradient of 0 however small the temperature (its difference from the largest logit, times
+    the parts of log2(e) / tau, leaves fp32 from 4e-8 on)."""
+    sts = cuda_lib
+    taus = torch.logspace(-30, -2, 141).tolist()
+    T, V = len(taus), 1003
+    z, _, gen = _rows(31, T, V, dtype, mask=mask)
+    tau = torch.tensor(taus)
+    tokens = torch.stack([z.argmax(1), torch.randint(V, (T,), generator=gen)], 1)
+    g, h = torch.randn(T, 2, generator=gen), torch.randn(T, generator=gen)
+    _, saved = sts.sts_token_logprobs(z.cuda(), tokens.cuda(), temperature=tau.cuda(), entropy=True, check=True)
+    dz = sts.sts_token_logprobs_backward(z.cuda(), tokens.cuda(), saved, g.cuda(), grad_entropy=h.cuda(), temperature=tau.cuda(),
+                                         out_dtype=torch.float32)
+    z64, tau64 = z.double().numpy(), tau.double().numpy()
+    ref = reference(z64, tau64, tokens.numpy(), 0)
+    want, tol = _grad_reference(z64, tau64, tokens.numpy(), 0, g.double().numpy(), h.double().numpy(), None, ref)
+    # a probability below 2^-126 is flushed: |G| + |h| (|ln p| + entropy) <= 8 + 4 (88 + 7), over tau
+    flush = np.where((ref["p"] > 0) & (ref["p"] < 2.0 ** -125), 2.0 ** -126 * 400, 0.0) / tau64[:, None]
+    err = np.abs(dz.double().cpu().numpy() - want)
+    lim = tol + U * (np.abs(want) + tol) + flush
+    bad = ~(err <= lim)
+    assert not bad.any(), (np.argwhere(bad)[:3], dz.cpu().numpy()[bad][:3], want[bad][:3], lim[bad][:3])
