@@ -923,13 +923,18 @@ struct RowCoef {
   float a, b;              // dz = p (a + b x)
 };
 
-__device__ __forceinline__ float grad_of(float z, const RowCoef& k) {
+// p and a + b x
+__device__ __forceinline__ float2 factors_of(float z, const RowCoef& k) {
   // c d comes first: where it leaves fp32 (masked tokens, low temperatures) x is
   // -inf whatever lo d is, or NaN, which fmaxf drops. Added to lo d, which may be
   // +inf, the exact product of the FMA would not count.
   const float d = z - k.zmax;
   const float x = fmaxf(fmaf(d, k.lo, fmaf(d, k.c, -k.l2s)), -200.f);
-  return ex2(x) * fmaf(k.b, x, k.a);
+  return make_float2(ex2(x), fmaf(k.b, x, k.a));
+}
+__device__ __forceinline__ float grad_of(float z, const RowCoef& k) {
+  const float2 f = factors_of(z, k);
+  return f.x * f.y;
 }
 
 template <typename T, typename O>
@@ -1017,8 +1022,18 @@ __global__ void __launch_bounds__(kThreads, 4) backward_kernel(const BwdArgs a) 
     k.c = (float)cd;
     k.lo = (float)(cd - (double)k.c);
     k.l2s = (float)((double)log_sum * kLog2eD);
-    k.a = (float)(-(sum + (h != 0.0 ? h * entropy : 0.0)) / (double)tau);
-    k.b = (float)(-h * kLn2 / (double)tau);
+    const double ca = -(sum + (h != 0.0 ? h * entropy : 0.0)) / (double)tau;
+    const double cb = -h * kLn2 / (double)tau;
+    k.a = (float)ca;
+    k.b = (float)cb;
+    // Temperatures below some 1e-36 take them out of fp32, where a probability of
+    // 0 would meet an infinity: 2^100 of them then goes over to p, by way of x
+    // (x + 100 is at most 100, and -200 still gives 0).
+    if (!(fabsf(k.a) + 200.f * fabsf(k.b) < 1e38f)) {
+      k.a = (float)((ca - 100.0 * cb) * 0x1p-100);
+      k.b = (float)(cb * 0x1p-100);
+      k.l2s -= 100.f;
+    }
   }
 
   for (int i0 = 0; i0 < body; i0 += kThreads * kUnroll) {
@@ -1065,7 +1080,10 @@ __global__ void __launch_bounds__(kThreads, 4) backward_kernel(const BwdArgs a) 
       }
       g += (double)sm.g[i];
     }
-    if (first) from_f32((float)(g / (double)tau + (double)grad_of(sm.z[j], k)), orow[id]);
+    if (first) {  // in float64: both terms may be beyond fp32 and their sum 0
+      const float2 f = factors_of(sm.z[j], k);
+      from_f32((float)(g / (double)tau + (double)f.x * (double)f.y), orow[id]);
+    }
   }
 }
 

@@ -577,3 +577,45 @@ def test_gradients_of_masked_tokens_at_low_temperatures(cuda_lib, dtype, mask):
     lim = tol + U * (np.abs(want) + tol) + flush
     bad = ~(err <= lim)
     assert not bad.any(), (np.argwhere(bad)[:3], dz.cpu().numpy()[bad][:3], want[bad][:3], lim[bad][:3])
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
+@pytest.mark.parametrize("V", [9, 5003, 40000])
+def test_gradients_at_the_smallest_temperatures(cuda_lib, dtype, V):
+    """Temperatures down to the smallest fp32: (G + h (ln p + entropy)) / tau leaves fp32, but a token without
+    probability has a gradient of 0 and the others theirs, infinite only where the formula's is beyond fp32."""
+    sts = cuda_lib
+    taus = [1e-30, 1e-35, 1e-36, 1e-37, 1e-38, 1e-40, 1.5e-45]
+    T, n = 3 * len(taus), 2
+    gen = torch.Generator().manual_seed(V)
+    z = torch.randn(T, V, generator=gen)
+    z[::3, 3] = 9.0
+    z[1::3, [2, V - 1]] = 9.0  # two equal ones
+    z[2::3] = -np.inf
+    z[2::3, V // 2] = 1.0
+    z = z.to(DTYPES[dtype])
+    tau = torch.tensor(taus).repeat_interleave(3)
+    tokens = torch.stack([z.argmax(1), torch.randint(V, (T,), generator=gen)], 1)
+    g, h, gt = torch.randn(T, 2, generator=gen), torch.randn(T, generator=gen), torch.randn(T, n, generator=gen)
+    zc = z.cuda()
+    lp, saved = sts.sts_token_logprobs(zc, tokens.cuda(), temperature=tau.cuda(), top_n=n, entropy=True)
+    assert (saved["flags"] == 0).all() and not torch.isnan(lp).any()
+    ref = reference(z.double().numpy(), tau.double().numpy(), tokens.numpy(), n)
+    most = {"fp32": torch.finfo(torch.float32).max, "bf16": torch.finfo(torch.bfloat16).max, "fp16": 65504.0}[dtype]
+    for hh, top in ((h, gt), (None, None)):
+        dz = sts.sts_token_logprobs_backward(zc, tokens.cuda(), saved, g.cuda(), grad_entropy=None if hh is None else hh.cuda(),
+                                             grad_top=None if top is None else top.cuda(), temperature=tau.cuda())
+        place = zc.clone()
+        sts.sts_token_logprobs_backward(place, tokens.cuda(), saved, g.cuda(), grad_entropy=None if hh is None else hh.cuda(),
+                                        grad_top=None if top is None else top.cuda(), temperature=tau.cuda(), out=place)
+        got = dz.double().cpu().numpy()
+        assert not np.isnan(got).any() and np.array_equal(place.double().cpu().numpy(), got)
+        want, tol = _grad_reference(z.double().numpy(), tau.double().numpy(), tokens.numpy(), n, g.double().numpy(),
+                                    None if hh is None else hh.double().numpy(), None if top is None else top.double().numpy(), ref)
+        lim = tol + HALF_STEP[dtype] * (np.abs(want) + tol)
+        inside = np.abs(want) + lim < most
+        with np.errstate(invalid="ignore"):
+            bad = inside & ~(np.abs(got - want) <= lim)
+        assert not bad.any(), (np.argwhere(bad)[:5], got[bad][:5], want[bad][:5], lim[bad][:5])
+        beyond = np.abs(want) - lim > 2 * most
+        assert (got[beyond] == np.sign(want[beyond]) * np.inf).all()
