@@ -802,6 +802,7 @@ _F32, _BF16, _F16 = torch.float32, torch.bfloat16, torch.float16
 _E4M3, _E5M2 = torch.float8_e4m3fn, torch.float8_e5m2
 _DTYPE_CODE = {_F32: 0, _BF16: 1, _F16: 2, _E4M3: 3, _E5M2: 4}
 _BLOCK = 128
+_MOST_TOP = 64  # alternatives per row
 
 
 def _raw_stream(index):
@@ -1005,8 +1006,8 @@ def sts_token_logprobs(logits, tokens=None, *, temperature=None, top_n=0, entrop
     lib = load()
     rows = _token_rows(logits, tokens, temperature, top_n)
     T, n = rows.T, rows.top_n
-    if n < 0:
-        raise StsError(STS_ERR_SHAPE, f"top_n must be 0 or more, got {n}")
+    if not 0 <= n <= _MOST_TOP:  # before anything of that size is allocated
+        raise StsError(STS_ERR_SHAPE, f"top_n must be 0 to {_MOST_TOP}, got {n}")
     index, elsewhere = _place(stream, (("logits", logits), ("tokens", tokens),
                                        ("temperature", temperature)))
     if elsewhere is not None:

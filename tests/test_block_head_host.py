@@ -226,6 +226,13 @@ def test_binding_refusals():
         sts.sts_token_logprobs(z, None, top_n=-1)
 
 
+@pytest.mark.parametrize("top_n", [-1, 65, 10 ** 9, 10 ** 12])
+def test_too_many_alternatives_are_refused_before_they_are_allocated(top_n):
+    with pytest.raises(sts.StsError) as e:
+        sts.sts_token_logprobs(torch.zeros(4, 100), None, top_n=top_n)
+    assert e.value.status == SHAPE and "top_n" in str(e.value)
+
+
 def test_the_bf16_entry_points_still_refuse_an_8_bit_head():
     H = torch.zeros(4, 64, dtype=torch.bfloat16)
     W = torch.zeros(100, 64, dtype=torch.float8_e4m3fn)
