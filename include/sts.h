@@ -408,7 +408,8 @@ typedef struct {
  * _BF16). With the hidden states as A and a head [V, d] as B it is the 8-bit
  * counterpart of sts_scaled_logits; the logits' gradient as A and the
  * transposed head as B give dH; the transposed gradient as A and the
- * transposed hidden states as B give dW. C's rows are ldc elements apart. It
+ * transposed hidden states as B give dW. C's rows are ldc elements apart, what lies
+ * behind their N elements is left as it is. It
  * must not overlap A, B or the scales. M = 0 and N = 0 are allowed. One kernel
  * launch, no scratch memory: ws may be NULL, or 256 bytes for the status word
  * that sts_get_status reads (STS_ERR_TIMEOUT). With or without it, what a

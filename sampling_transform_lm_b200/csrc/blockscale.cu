@@ -108,7 +108,7 @@ struct ProductArgs {
   int64_t ldc;
   int accumulate;
   int split;            // CTAs per tile (cluster size)
-  int tma_out;          // C can be written by TMA (wide)
+  int tma_cols;         // columns of C in the pieces that TMA writes (wide; 0: none)
   int give_up;          // a block that acts as if its first wait had given up, or -1
   int* err;
 };
@@ -397,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0 && lane == 0) {
     tma_prefetch_desc(&map_l);
     tma_prefetch_desc(&map_c);
-    if (kWide && p.tma_out) tma_prefetch_desc(&map_out);
+    if (kWide && p.tma_cols > 0) tma_prefetch_desc(&map_out);
   }
   if (warp == 1) {
     tmem_alloc(smem_u32(tmem_holder), S::kTmemCols);
@@ -765,7 +765,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
               st_shared_v4(buf_s + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4), w[0], w[1], w[2], w[3]);
             }
-            if (p.tma_out) {
+            if (n0 < p.tma_cols) {
               fence_proxy_async_smem();
               __syncwarp();
               if (lane == 0) {
@@ -775,7 +775,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                   tma_store_2d(&map_out, buf_s, n0, m0);
                 bulk_commit();
               }
-            } else {  // rows of C that TMA cannot address: 64 bytes of a row per 16 or 32 lanes
+              sel ^= 1u;  // (the other way's piece has been read when its turn is over)
+            } else {  // what TMA cannot address of C: 64 bytes of a row per 16 or 32 lanes
               __syncwarp();
               constexpr int kRows = 32 / kCols;  // rows per step
               const int col = lane % kCols;
@@ -787,7 +788,6 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
               __syncwarp();
             }
-            sel ^= 1u;
           }
         }
       }
@@ -1061,7 +1061,10 @@ extern "C" sts_status sts_block_scaled_product(const sts_block_operand* A,
                        (uint64_t)N, (uint64_t)M, (uint64_t)(ldc * cs), (uint32_t)(64 / cs), 32,
                        CU_TENSOR_MAP_SWIZZLE_64B))
       return STS_ERR_CUDA;
-    p.tma_out = 1;
+    // TMA ends a row at whole 16 bytes: the last piece of rows that end elsewhere
+    // would reach over what lies behind them
+    const int64_t piece = 64 / cs;
+    p.tma_cols = (int)(N * cs % 16 == 0 ? N : N / piece * piece);
   }
   const LaunchMark mark = launch_begin(STS_KERNEL_BLOCK_PRODUCT, st);
   const cudaError_t e = bf ? launch_out<__nv_bfloat16>(NT, uniform, maps, p, grid, st)

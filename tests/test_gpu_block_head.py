@@ -214,6 +214,29 @@ def test_product_strides_accumulation_and_neighbours(cuda_lib, M, N, K):
     assert (rest == 5.0).all()
 
 
+@pytest.mark.parametrize("out", ["fp32", "bf16"])
+@pytest.mark.parametrize("M,N", [(300, 739), (129, 3), (1000, 2049), (700, 5003), (40, 501), (300, 256), (200, 777)])
+@pytest.mark.parametrize("K", [130, 9000])  # whole, and split over k where there are few tiles
+@pytest.mark.parametrize("more", [1, 2, 5, 8])
+def test_product_leaves_what_lies_behind_a_row(cuda_lib, out, M, N, K, more):
+    """Rows of C that start on 16-byte boundaries and end anywhere: the bytes up to the next row keep their values."""
+    gen = torch.Generator().manual_seed(N)
+    A, sa = _operand(gen, M, K, E4M3, 1)
+    B, sb = _operand(gen, N, K, E4M3, 128)
+    ld = -(-(N + more) // 8) * 8
+    plain = cuda_lib.sts_block_scaled_product(A, sa, B, sb, out_dtype=SRC[out])
+    want, size = _product_reference(A, sa, B, sb, 128)
+    assert ((plain.double() - want).abs() <= _product_tol(want, size, K, SRC[out])).all()
+    for accumulate in (False, True) if out == "fp32" else (False,):
+        held = torch.full((M + 1, ld), -3.0, dtype=SRC[out], device="cuda")
+        got = held[:M, :N]
+        if accumulate:
+            got.zero_()
+        cuda_lib.sts_block_scaled_product(A, sa, B, sb, out=got, accumulate=accumulate)
+        assert torch.equal(got, plain)
+        assert (held[:M, N:] == -3).all() and (held[M] == -3).all()
+
+
 @pytest.mark.parametrize("M,N,K", [(40, 300, 9000), (300, 400, 9000)])
 def test_product_split_over_k_accumulates_and_fits_any_rows(cuda_lib, M, N, K):
     """A cluster per tile, both forms: C off any alignment, added to, its neighbours left alone."""
