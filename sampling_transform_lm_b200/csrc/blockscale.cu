@@ -197,10 +197,8 @@ __device__ __forceinline__ void copies_arrive(uint32_t bar) {
 // 32 lanes x kN consecutive columns of tensor memory; complete after tmem_wait.
 template <int kN>
 __device__ __forceinline__ void tmem_ld(uint32_t taddr, uint32_t (&r)[kN]) {
-  static_assert(kN == 8 || kN == 16 || kN == 32, "");
-  if constexpr (kN == 32) {
-    tmem_ld_32x32b_x32(taddr, r);
-  } else if constexpr (kN == 8) {
+  static_assert(kN == 8 || kN == 16, "");
+  if constexpr (kN == 8) {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
                    "=r"(r[6]), "=r"(r[7])
@@ -594,7 +592,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int j = 0; j < kHalf / 2; ++j) acc[j] = 0;
       constexpr int kPer = kHalf / kChunk, kSteps = kG * kPer;
       if constexpr (kG == 1) {
-        // a block at a time, the next 16 columns on their way while 16 are summed
+        // a block at a time, the next kChunk columns on their way while kChunk are summed
         uint32_t r[2][kChunk];
         for (int kb = kb0; kb < kb1; ++kb) {
           if (!mbar_wait_soon(smem_u32(&sfull[slot]), sphase, abort_flag, p.err)) {
@@ -648,6 +646,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // A group's columns in steps of kChunk, two steps from tensor memory at a
         // time: the next one is on its way while one is summed.
         static_assert(kSteps % 2 == 0, "steps go in pairs");
+        static_assert(!kUniform, "groups are the narrow form's: every column has a scale of its own");
         uint32_t r[2][kChunk];
         const uint32_t lane_addr = tmem_base + ((uint32_t)(quarter * 32) << 16) + half * kHalf;
         for (int kb = kb0; kb < kb1; kb += kG) {
@@ -661,23 +660,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           };
           load(0);
           load(1);
-          float sl[kG], sc[kUniform ? kG : 1];
+          float sl[kG];
 #pragma unroll
           for (int g = 0; g < kG; ++g) {
             const float* at = sS + slot * (S::kSlot / 4) + g * S::kBlockScales;
             sl[g] = at[quarter * 32 + lane];
-            if constexpr (kUniform) sc[g] = at[kLanes + half];
           }
 #pragma unroll
           for (int st = 0; st < kSteps; ++st) {
             const int g = st / kPer, c = st % kPer;
-            float4 b[kUniform ? 1 : kChunk / 4];
-            if constexpr (!kUniform) {  // on their way while tensor memory answers
-              const float* at = sS + slot * (S::kSlot / 4) + g * S::kBlockScales + kLanes + half * kHalf;
+            float4 b[kChunk / 4];  // on their way while tensor memory answers
+            const float* at = sS + slot * (S::kSlot / 4) + g * S::kBlockScales + kLanes + half * kHalf;
 #pragma unroll
-              for (int j = 0; j < kChunk / 4; ++j)
-                b[j] = *reinterpret_cast<const float4*>(at + c * kChunk + 4 * j);
-            }
+            for (int j = 0; j < kChunk / 4; ++j)
+              b[j] = *reinterpret_cast<const float4*>(at + c * kChunk + 4 * j);
             if (st % 2 == 0) {
               tmem_wait<kChunk>(r[0]);
               tmem_tie<kChunk>(r[1]);
@@ -688,10 +684,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
             }
             if (g < live) {
-              const float s = kUniform ? sl[g] * sc[kUniform ? g : 0] : sl[g];
-              const uint64_t s2 = pair(s, s);
+              const uint64_t s2 = pair(sl[g], sl[g]);
               uint32_t(&w)[kChunk] = r[st & 1];
-              sum_columns<kUniform, kChunk>(acc + c * kChunk / 2, w, b, s2);
+              sum_columns<false, kChunk>(acc + c * kChunk / 2, w, b, s2);
             }
             if (st + 2 < kSteps) load(st + 2);
           }
