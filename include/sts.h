@@ -408,13 +408,14 @@ typedef struct {
  * _BF16). With the hidden states as A and a head [V, d] as B it is the 8-bit
  * counterpart of sts_scaled_logits; the logits' gradient as A and the
  * transposed head as B give dH; the transposed gradient as A and the
- * transposed hidden states as B give dW. C's rows are ldc elements apart, what lies
- * behind their N elements is left as it is. It
- * must not overlap A, B or the scales. M = 0 and N = 0 are allowed. One kernel
- * launch, no scratch memory: ws may be NULL, or 256 bytes for the status word
- * that sts_get_status reads (STS_ERR_TIMEOUT). With or without it, what a
- * device-side wait that gave up leaves unknown of C is NaN. The result depends on the shapes and the
- * device's SM count, not on what else runs. */
+ * transposed hidden states as B give dW. C's rows are ldc elements apart; what
+ * lies behind their N elements is left as it is. C must not overlap A, B or the
+ * scales. M = 0 and N = 0 are allowed. One kernel launch, no scratch memory: ws
+ * may be NULL, or 256 bytes for the status word that sts_get_status reads
+ * (STS_ERR_TIMEOUT). With or without it, what a device-side wait that gave up
+ * leaves unknown of C is NaN. The result depends on the shapes and the device
+ * (its SMs, and the thread block clusters that it holds at once), not on what
+ * else runs. */
 sts_status sts_block_scaled_product(const sts_block_operand* A, const sts_block_operand* B,
                                     int64_t K, const float* temperature, void* C, int c_dtype,
                                     int64_t ldc, int accumulate, void* ws, size_t ws_bytes,

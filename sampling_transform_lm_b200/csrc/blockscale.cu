@@ -938,6 +938,38 @@ bool wide_form(int64_t M, int64_t N, int64_t kb, int sms) {
 // 8 rows 22, with 32 rows 20.
 constexpr int kMinHeight = 16;
 
+// Clusters of `size` blocks that the current device holds at once. A block takes
+// an SM whatever its form, and a cluster lies within one of the device's groups of
+// SMs, so there are fewer than sms / size: 74 of 2, 33 of 4 and 15 of 8 on a B200
+// of 148 SMs.
+int clusters_held(int size, int sms) {
+  constexpr int kDevices = 64;
+  static std::atomic<int> held[kDevices][kMaxSplit + 1];
+  int device = 0;
+  if (cudaGetDevice(&device) != cudaSuccess || device >= kDevices) return sms / size;
+  int n = held[device][size].load(std::memory_order_relaxed);
+  if (n > 0) return n;
+  using S = Shape<256, true, true>;
+  auto kern = product_kernel<256, true, true, float>;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)size);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = S::kSmem;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)size;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem) !=
+          cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1)
+    return sms / size;
+  held[device][size].store(n, std::memory_order_relaxed);
+  return n;
+}
+
 sts_status check_operand(const sts_block_operand* o, int64_t K, bool rows_only) {
   if (!o) return STS_ERR_NULL;
   if (o->dtype != STS_DTYPE_E4M3 && o->dtype != STS_DTYPE_E5M2) return STS_ERR_DTYPE;
@@ -1025,10 +1057,15 @@ extern "C" sts_status sts_block_scaled_product(const sts_block_operand* A,
   p.accumulate = accumulate ? 1 : 0;
   p.give_up = (int)g_give_up.load(std::memory_order_relaxed);
   const int64_t tiles = tiles_l * tiles_c;
-  // a stretch of k for each of 2, 4 or 8 CTAs while the SMs are not full, none
-  // below 4 blocks (300 x 2,048 x 8,192: 25 us, whole 39; 1 x 512 x 16,384: 16, 31)
+  // a stretch of k for each of 2, 4 or 8 CTAs while the device holds all tiles'
+  // clusters at once, none below 4 blocks. 300 x 512 x 16,384 (6 tiles): 8 parts
+  // 18.5 us, 4 24.7, whole 61.5; 300 x 2,048 x 8,192 (24): 4 parts 18.6, 2 26.8,
+  // whole 35.2. Where the last clusters would wait for the first, 1 x 256 x 16,384
+  // (16): 4 parts 12.4, 8 16.5; 300 x 1,536 x 16,384 (18): 4 parts 26.7, 8 34.1
   p.split = 1;
-  while (p.split < kMaxSplit && tiles * p.split * 2 <= sms && p.kb >= p.split * 2 * 4) p.split *= 2;
+  while (p.split < kMaxSplit && tiles * p.split * 2 <= sms && p.kb >= p.split * 2 * 4 &&
+         tiles <= clusters_held(p.split * 2, sms))
+    p.split *= 2;
   const int grid = (int)(p.split > 1 ? tiles * p.split : (tiles < sms ? tiles : sms));
 
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);

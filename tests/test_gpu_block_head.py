@@ -214,6 +214,20 @@ def test_product_strides_accumulation_and_neighbours(cuda_lib, M, N, K):
     assert (rest == 5.0).all()
 
 
+@pytest.mark.parametrize("M", [1, 300])
+@pytest.mark.parametrize("tiles", [1, 15, 16, 17, 18, 19, 33, 34, 37, 38, 74, 75])
+def test_product_around_the_clusters_that_the_device_holds(cuda_lib, M, tiles):
+    """Few tiles and a long k: from 8 parts a tile to none, in both forms (16 rows of B a tile, or 128 x 256)."""
+    N, K = (tiles * 16, 4200) if M == 1 else (max(1, tiles // 3) * 256, 4200)
+    gen = torch.Generator().manual_seed(tiles)
+    A, sa = _operand(gen, M, K, E4M3, 1)
+    B, sb = _operand(gen, N, K, E4M3, 128)
+    C = cuda_lib.sts_block_scaled_product(A, sa, B, sb, check=True)
+    want, size = _product_reference(A, sa, B, sb, 128)
+    assert ((C.double() - want).abs() <= _product_tol(want, size, K, torch.float32)).all()
+    assert torch.equal(C, cuda_lib.sts_block_scaled_product(A, sa, B, sb))
+
+
 @pytest.mark.parametrize("out", ["fp32", "bf16"])
 @pytest.mark.parametrize("M,N", [(300, 739), (129, 3), (1000, 2049), (700, 5003), (40, 501), (300, 256), (200, 777)])
 @pytest.mark.parametrize("K", [130, 9000])  # whole, and split over k where there are few tiles
