@@ -920,15 +920,22 @@ constexpr int64_t kMost = (int64_t(1) << 31) - 1024;
 
 std::atomic<int64_t> g_give_up{-1};  // sts_probe_product_timeout
 
-// Which form. Above 128 rows of A the wide one, up to 64 the narrow one; between
-// them by the rounds of tiles that each takes over the SMs. A round of the wide
-// form's tiles takes about as long as its blocks along k and 12 more (its results
-// leave while nothing is multiplied), of the narrow form's as its blocks and 2
-// more. 70 x 21,000 x 4,096: wide 33 us, narrow 51; 100 x 151,936 x 4,096: 145
-// and 207; 77 x 50,021 x 2,048: 57 and 47; 128 x 2,048 x 2,048: 27 and 21.
-bool wide_form(int64_t M, int64_t N, int64_t kb, int sms) {
+// Which form. Above 128 rows of A the wide one, up to 64 the narrow one (33 to 64
+// rows: as fast as each other at the median of 207 shapes where TMA can write C,
+// the narrow one 1.6 times where it cannot). Between them the wide
+// one where TMA can: of 276 shapes it took 0.7 of the narrow one's time at
+// the median (128 x 2,048 x 2,048 12.4 us, narrow 18.5; 100 x 151,936 x 4,096 125,
+// narrow 202; 96 x 8,000 x 8,192 22.5, narrow 43.7), more only where there is little
+// work (128 x 300 x 1,024 14.4, narrow 12.4). Where C leaves by ordinary stores, by
+// the rounds of tiles that each takes over the SMs: a round of the wide form's
+// takes about as long as its blocks along k and 12 more (its results leave while
+// nothing is multiplied), of the narrow form's as its blocks and 2 more. 77 x
+// 50,021 x 2,048: wide 49.1, narrow 43.1; x 4,096 68.0 and 70.5; x 8,192 106 and
+// 121.
+bool wide_form(int64_t M, int64_t N, int64_t kb, int sms, bool tma) {
   if (M > 128) return true;
   if (M <= 64) return false;
+  if (tma) return true;
   const int64_t wide = ((N + 255) / 256 + sms - 1) / sms;
   const int64_t narrow = (N + (int64_t)kLanes * sms - 1) / ((int64_t)kLanes * sms);
   return wide * (kb + 12) < narrow * (kb + 2);
@@ -1020,7 +1027,11 @@ extern "C" sts_status sts_block_scaled_product(const sts_block_operand* A,
   if (s != STS_OK) return s;
 
   const int64_t M = A->rows, N = B->rows;
-  const bool wide = wide_form(M, N, (K + kBlock - 1) / kBlock, sms);
+  const bool bf = c_dtype == STS_DTYPE_BF16;
+  const int64_t cs = bf ? 2 : 4;
+  const bool tma = (reinterpret_cast<uintptr_t>(C) & 15u) == 0 && ldc * cs % 16 == 0 &&
+                   ldc < (int64_t(1) << 37);  // it can address C's rows
+  const bool wide = wide_form(M, N, (K + kBlock - 1) / kBlock, sms, tma);
   const int NT = wide ? 256 : M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
   const sts_block_operand* L = wide ? A : B;  // the lanes' operand
   const sts_block_operand* R = wide ? B : A;  // the columns'
@@ -1076,8 +1087,6 @@ extern "C" sts_status sts_block_scaled_product(const sts_block_operand* A,
       return STS_ERR_CUDA;
     p.err = &hdr->err;
   }
-  const bool bf = c_dtype == STS_DTYPE_BF16;
-  const int64_t cs = bf ? 2 : 4;
   Maps maps;
   std::memset(&maps, 0, sizeof(maps));
   if (!tensor_map_2d(&maps.lanes, L->q, CU_TENSOR_MAP_DATA_TYPE_UINT8, (uint64_t)K,
@@ -1087,8 +1096,7 @@ extern "C" sts_status sts_block_scaled_product(const sts_block_operand* A,
                      (uint64_t)R->rows, (uint64_t)R->ld, kBlock, (uint32_t)NT,
                      CU_TENSOR_MAP_SWIZZLE_128B))
     return STS_ERR_CUDA;
-  if (wide && (reinterpret_cast<uintptr_t>(C) & 15u) == 0 && ldc * cs % 16 == 0 &&
-      ldc < (int64_t(1) << 37)) {
+  if (wide && tma) {
     if (!tensor_map_2d(&maps.out, C, bf ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32,
                        (uint64_t)N, (uint64_t)M, (uint64_t)(ldc * cs), (uint32_t)(64 / cs), 32,
                        CU_TENSOR_MAP_SWIZZLE_64B))
