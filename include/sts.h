@@ -400,8 +400,8 @@ typedef struct {
 
 /* C [M, N] = A [M, K] . B [N, K]^T, each block of 128 along K scaled in fp32:
  *   C[m, n] = sum_kb a[m, kb] b[n, kb] sum_{k in kb} A[m, k] B[n, k]
- * (tensor-core products and sums of a block in fp32, blocks summed in fp32
- * registers in increasing k), then multiplied by 1 / temperature[m] where that
+ * (tensor-core products and sums of a block in fp32; a b, rounded to fp32, times
+ * each, and blocks summed, in fp32 registers in increasing k), then multiplied by 1 / temperature[m] where that
  * is given (the reciprocal rounded to fp32; not validated: sts_resolve_logits
  * and sts_token_logprobs check the rows' temperatures), then added to C where
  * accumulate is set (fp32 C only), then rounded to c_dtype (STS_DTYPE_F32 or

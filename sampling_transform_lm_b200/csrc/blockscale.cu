@@ -34,13 +34,16 @@
 // cluster of 2, 4 or 8 CTAs shares a tile: each takes a stretch of k, the sums
 // meet in distributed shared memory and are added in the order of k.
 //
-// What bounds it. Narrow: HBM. 1 x 151,936 x 4,096 takes 96 us back to back, 6.45
-// TB/s, 98 % of a measured copy; 77 x 50,021 x 2,048 43 us, 2.6 times its bytes,
-// where three rounds of tiles of 16 blocks each end in a write of C. Wide: the
-// sums. 4,096 x 152,064 x 5,120 takes 3.25 ms (1.96 PFLOP/s) for 5,160 blocks an
-// SM, 0.63 us a block. Alone, the products take 0.29 us of that, the loads 0.26,
-// both together 0.37 (they share the bandwidth of shared memory), reading tensor
-// memory and handing blocks over 0.34, the FMAs 0.12 more, the writing of C 10 %.
+// What bounds it. Narrow: HBM. 1 x 151,936 x 4,096 takes 93 to 97 us, 6.4 to 6.7
+// TB/s; 77 x 50,021 x 2,048 43 us, 2.6 times its bytes, where three rounds of
+// tiles of 16 blocks each end in a write of C. Wide: the sums. 4,096 x 152,064 x
+// 5,120 takes 3.16 to 3.19 ms in a short burst at full clocks (2.0 PFLOP/s), 3.6
+// to 3.7 back to back under the power cap (1.7 to 1.8), for 5,160 blocks an SM,
+// 0.61 us a block in the burst. Alone, the products take 0.29 us of a block, the
+// loads 0.26, both together 0.37 (they share the bandwidth of shared memory),
+// reading tensor memory and handing blocks over 0.34, the FMAs 0.12 more, the
+// writing of C 10 %. With a scale per row of both, 32,768 x 2,048 x 4,001 takes 435
+// to 446 us in a burst, 490 to 510 back to back; that form spills 12 bytes.
 // Sixteen warps of sums (96 registers), 32 columns a read (spills) and waiting by
 // polling were each slower by 1 to 20 %.
 #include <atomic>
@@ -69,7 +72,7 @@ struct Shape {
   static_assert(!kUniform || kWide, "a uniform column scale is the wide form's");
   // blocks that change hands together: the accumulators of a group are waited
   // for, read and given back at once (a handover costs the sums some 300 clocks:
-  // 1 x 2,368 x 65,536 took 174 us block by block, 107 by fours)
+  // 1 x 2,368 x 65,536 took 174 us block by block, by fours it takes 98)
   static constexpr int kGroupBlocks = kWide ? 1 : NT == 128 ? 2 : 4;
   static constexpr int kBufs = 2;  // groups of accumulators
   static constexpr uint32_t kTmemCols = NT * kGroupBlocks * kBufs;
@@ -920,18 +923,19 @@ constexpr int64_t kMost = (int64_t(1) << 31) - 1024;
 
 std::atomic<int64_t> g_give_up{-1};  // sts_probe_product_timeout
 
-// Which form. Above 128 rows of A the wide one, up to 64 the narrow one (33 to 64
-// rows: as fast as each other at the median of 207 shapes where TMA can write C,
-// the narrow one 1.6 times where it cannot). Between them the wide
-// one where TMA can: of 276 shapes it took 0.7 of the narrow one's time at
-// the median (128 x 2,048 x 2,048 12.4 us, narrow 18.5; 100 x 151,936 x 4,096 125,
-// narrow 202; 96 x 8,000 x 8,192 22.5, narrow 43.7), more only where there is little
-// work (128 x 300 x 1,024 14.4, narrow 12.4). Where C leaves by ordinary stores, by
-// the rounds of tiles that each takes over the SMs: a round of the wide form's
-// takes about as long as its blocks along k and 12 more (its results leave while
-// nothing is multiplied), of the narrow form's as its blocks and 2 more. 77 x
-// 50,021 x 2,048: wide 49.1, narrow 43.1; x 4,096 68.0 and 70.5; x 8,192 106 and
-// 121.
+// Which form. Above 128 rows of A the wide one, up to 64 the narrow one (at 33 to
+// 64 rows the two take the same time at the median of 207 shapes where TMA can
+// write C; where it cannot, the wide one takes 1.6 times the narrow one's). Between
+// them the wide one where TMA can: it took 0.7 of the narrow one's time at the
+// median of 276 shapes (128 x 2,048 x 2,048 12.4 us, narrow 18.5; 100 x 151,936 x
+// 4,096 125, narrow 202; 96 x 8,000 x 8,192 22.5, narrow 43.7), more only where
+// there is little work (128 x 300 x 1,024 14.4, narrow 12.4). Where C leaves by
+// ordinary stores, by the rounds of tiles that each takes over the SMs: a round of
+// the wide form's takes about as long as its blocks along k and 12 more (its
+// results leave while nothing is multiplied), of the narrow form's as its blocks
+// and 2 more. 77 x 50,021 x 2,048: wide 49.1, narrow 43.1; x 4,096 68.0 and 70.5; x
+// 8,192 106 and 121 (with a scale per row of B x 4,096 83 and 70: there the wide
+// form's blocks cost more than the estimate has it).
 bool wide_form(int64_t M, int64_t N, int64_t kb, int sms, bool tma) {
   if (M > 128) return true;
   if (M <= 64) return false;
@@ -941,8 +945,8 @@ bool wide_form(int64_t M, int64_t N, int64_t kb, int sms, bool tma) {
   return wide * (kb + 12) < narrow * (kb + 2);
 }
 
-// Rows of B in the narrow form's smallest tile: 1 x 512 x 16,384 takes 16 us, with
-// 8 rows 22, with 32 rows 20.
+// Rows of B in the narrow form's smallest tile: 1 x 512 x 16,384 takes 13.4 us, with
+// 32 rows 16.5 (with 64, and 8 parts a tile, 10.3).
 constexpr int kMinHeight = 16;
 
 // Clusters of `size` blocks that the current device holds at once. A block takes
@@ -1045,7 +1049,8 @@ extern "C" sts_status sts_block_scaled_product(const sts_block_operand* A,
   p.height = kLanes;
   if (!wide) {
     // as many rounds of tiles as 128 rows each would take, and equal tiles (1 x
-    // 2,048 x 4,096: 14 us, with tiles of 128 rows 18; 1 x 32,768 x 4,096: 35, 37)
+    // 32,768 x 4,096: 26.4 us, with tiles of 64 rows 31.0, of 16 89.0; 1 x 2,048 x
+    // 4,096: 12.4, of 64 rows and 4 parts 9.1, of 128 12.4)
     const int64_t rounds = (N + (int64_t)kLanes * sms - 1) / ((int64_t)kLanes * sms);
     p.height = (int)((N + rounds * sms - 1) / (rounds * sms));
     if (p.height < kMinHeight) p.height = kMinHeight;

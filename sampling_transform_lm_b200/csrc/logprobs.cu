@@ -45,10 +45,13 @@
 // vocabulary; the first block joins their results over distributed shared
 // memory. One launch, no workspace, nothing shared between calls.
 //
-// What it takes. The gradient: 4,096 rows of 152,064 bf16 logits 397 us, 6.27
-// TB/s, 96 % of a measured copy. The forward: the same rows 281 us without
-// alternatives, 307 with 8, 453 with 64 (HBM: 190); 2,048 rows of 151,936 fp32 with
-// 20 270 (190). It issues 2.7 to 3 instructions a clock (some 10 an element, and
+// What it takes. The gradient: 4,096 rows of 152,064 bf16 logits 390 us in short
+// bursts, 398 to 416 back to back (6.0 to 6.4 TB/s, 91 to 97 % of a measured copy);
+// to fp32 645 to 655 (6.9 GB; the form spills 32 bytes). Rows of logits and result
+// on different 16-byte boundaries: 555 for types of one width, 2,100 for bf16 to
+// fp32, whose elements are then stored one by one. The forward: the same rows 275 to
+// 290 us without alternatives, 303 to 315 with 8, 451 with 64 (HBM: 190); 2,048
+// rows of 151,936 fp32 with 20 258 to 276 (190). It issues 2.7 to 3 instructions a clock (some 10 an element, and
 // one exponential, which alone would take as long as the bytes do); 64
 // alternatives cost 2,400 instructions a row and warp more, in ranking them at
 // each doubling of the row. Packed fp32 operations lost more in moves than they
@@ -75,9 +78,10 @@ constexpr int kMaxGiven = 512;   // given tokens per row
 constexpr int kMaxParts = 8;     // portable cluster size
 constexpr int kKeyCap = 1024;    // keys kept between two tightenings
 // Rows up to this long have blocks of 128 threads, so that more of them are in
-// flight: 500 rows of 30,000 bf16 take 35 us (256 threads: 39), 8,192 rows of
-// 1,024 fp32 66 us (107); one row of 151,936 fp32 35 us (25), 4,096 rows of
-// 152,064 bf16 the same.
+// flight: 8,192 rows of 1,024 fp32 take 62 us (256 threads: 104), of 16,000 bf16 101
+// (123); one row of 151,936 fp32 23 us (18.5), 4,096 rows of 152,064 bf16 the same.
+// A few hundred rows of tens of thousands would be faster with 256 threads (500 of
+// 30,000 bf16: 24.7 us, 20.5).
 constexpr int64_t kShortRow = 65536;
 constexpr double kLog2eD = 1.4426950408889634074;
 constexpr double kLn2 = 0.69314718055994530942;
@@ -1092,11 +1096,13 @@ __global__ void __launch_bounds__(kThreads, 4) backward_kernel(const BwdArgs a) 
 // Parts per row: 1, 2, 4 or 8, none much shorter than one round of the loop; a
 // block's cost is its bytes and 32 KB more. The gradient and the forward's short
 // rows: as many waves of blocks as there are, four (of 128 threads seven) an SM:
-// 700 rows of 152,064 bf16, gradient, 2 parts 90 us, 1 part 102; 400 rows 1 part
-// 57, 2 parts 61; 333 rows of 32,771 fp32, forward, 2 parts 39, 4 parts 53. The
-// forward's long rows are bound by instructions: as many blocks as the busiest SM
-// gets, the slower the fewer threads that SM has: 100 rows of 152,064 bf16 4 parts
-// 29 us, 8 parts 37; 400 rows 2 parts 57, 1 part 70; 700 rows 1 part 78, 2 parts 109.
+// 700 rows of 152,064 bf16, gradient, 4 parts 80.8 us, 2 82.6, 1 89.8; 400 rows 4
+// parts 50.0, 1 49.2, 2 56.8; 333 rows of 32,771 fp32, forward, 2 parts 28.7, 4
+// 39.9. The forward's long rows are bound by instructions: as many blocks as the
+// busiest SM gets, the slower the fewer threads that SM has: 100 rows of 152,064
+// bf16 4 parts 23 us, 8 31, 2 25; 700 rows 1 part 70, 2 82. Of some 200 to 500 rows it
+// divides too many (400 rows: 2 parts 54.5 us, 1 part 45.2): over 762 shapes the
+// forward takes 1.12 of the best choice's time, 1.9 at most.
 int parts_for(int64_t T, int64_t V, int elem, int sms, int threads, bool forward) {
   const int64_t round = (int64_t)threads * kUnroll * (16 / elem);
   int best = 1;

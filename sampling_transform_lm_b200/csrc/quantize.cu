@@ -9,8 +9,11 @@
 //           limited to +-top, rounded to nearest even in the 8-bit type; NaN for
 //           an x that is not finite
 // (a division an element would be bound by its instructions, not by HBM: 1.29
-// ms for 151,936 x 4,096 bf16), so that code * scale is x within half a step of the 8-bit type (2^-4
-// relative for e4m3 in its normal range). Entries that are not finite do not
+// ms for 151,936 x 4,096 bf16), so that code * scale is x within half a step of
+// the 8-bit type (2^-4 relative for e4m3 in its normal range). The reciprocal's
+// rounding shows where x / scale lies within 2^-23 of the middle between two
+// codes, as quotients of bf16 values often do: 0.05 % of the codes of 151,936 x
+// 4,096 are then the other neighbour. Entries that are not finite do not
 // enter the scale, so they cost their neighbours no precision, and stay
 // visible as NaN in every product that they take part in.
 //
@@ -25,11 +28,13 @@
 //   cols     x's rows are contiguous (a transposed view): 256 threads hold 128
 //            x 128 elements; the codes cross shared memory, so that both the
 //            reads along x's rows and the writes along K are whole lines.
-// 151,936 x 4,096 bf16 takes 330 us in either block (5.7 TB/s, 86 % of a measured
-// copy), fp32 32,768 x 4,096 107 us (6.3 TB/s); rows that are no multiple of 16
-// bytes are read element by element (32,768 x 4,001 fp32: 168 us). cols holds two
-// to three thread blocks an SM, too few to hide its three barriers: 32,768 x
-// 4,001 bf16, transposed, 93 us (4.2 TB/s).
+// 151,936 x 4,096 bf16 takes 319 to 330 us in 1 x 128 blocks, 326 to 350 in 128 x
+// 128 (5.3 to 5.9 TB/s, 81 to 90 % of a measured copy), fp32 32,768 x 4,096 97 us;
+// rows that are no multiple of 16 bytes are read element by element (32,768 x
+// 4,001: fp32 166 us, bf16 168). cols holds two to three thread blocks an SM, too
+// few to hide its three barriers: 32,768 x 4,001, transposed, bf16 90 to 94 us
+// (4.2 to 4.4 TB/s), in 128 x 128 blocks 85, fp32 127, fp16 104 (its 1 x 128 form
+// spills some 120 bytes).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
