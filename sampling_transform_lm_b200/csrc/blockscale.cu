@@ -975,8 +975,10 @@ int clusters_held(int size, int sms) {
   cfg.numAttrs = 1;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem) !=
           cudaSuccess ||
-      cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1)
+      cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) {
+    cudaGetLastError();  // the launch does not answer for it
     return sms / size;
+  }
   held[device][size].store(n, std::memory_order_relaxed);
   return n;
 }
