@@ -1055,25 +1055,34 @@ def sts_token_logprobs_backward(logits, tokens, saved, grad_logprob=None, *, gra
     ``out`` may be ``logits`` itself. Tokens of -1, masked tokens, and empty or invalid rows
     contribute nothing."""
     lib = load()
-    top_id = saved["top_id"] if grad_top is not None else None
+    get = saved.get
+    logit_max, log_sum, flags = get("logit_max"), get("log_sum"), get("flags")
+    entropy = None if grad_entropy is None else get("entropy")
+    top_id = None if grad_top is None else get("top_id")
+    if (logit_max is None or log_sum is None or flags is None
+            or (entropy is None and grad_entropy is not None)
+            or (top_id is None and grad_top is not None)):
+        needed = (("logit_max", True), ("log_sum", True), ("flags", True),
+                  ("entropy", grad_entropy is not None), ("top_id", grad_top is not None))
+        lacks = ", ".join(k for k, need in needed if need and get(k) is None)
+        raise StsError(STS_ERR_NULL, f"saved lacks {lacks}")
     rows = _token_rows(logits, tokens, temperature, 0 if top_id is None else top_id.shape[1])
     T, V = rows.T, rows.V
     for name, t, dtype, shape in (
-            ("logit_max", saved["logit_max"], _F32, (T,)), ("log_sum", saved["log_sum"], _F32, (T,)),
-            ("flags", saved["flags"], torch.int32, (T,)),
+            ("logit_max", logit_max, _F32, (T,)), ("log_sum", log_sum, _F32, (T,)),
+            ("flags", flags, torch.int32, (T,)),
             ("grad_logprob", grad_logprob, _F32, None if tokens is None else tokens.shape),
             ("grad_entropy", grad_entropy, _F32, (T,)),
-            ("entropy", None if grad_entropy is None else saved["entropy"], _F32, (T,)),
+            ("entropy", entropy, _F32, (T,)),
             ("grad_top", grad_top, _F32, None if top_id is None else top_id.shape),
             ("top_id", top_id, torch.int64, (T, rows.top_n))):
         if t is not None and (t.dtype != dtype or t.shape != shape or not t.is_contiguous()):
             raise StsError(STS_ERR_SHAPE, f"{name} must be contiguous {dtype} "
                                           f"{None if shape is None else tuple(shape)}, got "
                                           f"{t.dtype} {tuple(t.shape)}")
-    entropy = None if grad_entropy is None else saved["entropy"]
     index, elsewhere = _place(stream, (
         ("logits", logits), ("tokens", tokens), ("temperature", temperature),
-        ("logit_max", saved["logit_max"]), ("log_sum", saved["log_sum"]), ("flags", saved["flags"]),
+        ("logit_max", logit_max), ("log_sum", log_sum), ("flags", flags),
         ("entropy", entropy), ("top_id", top_id), ("grad_logprob", grad_logprob),
         ("grad_entropy", grad_entropy), ("grad_top", grad_top), ("out", out)))
     if elsewhere is not None:
@@ -1087,8 +1096,8 @@ def sts_token_logprobs_backward(logits, tokens, saved, grad_logprob=None, *, gra
             V > 1 and out.stride(1) != 1):
         raise StsError(STS_ERR_SHAPE, f"out must be {(T, V)} with contiguous rows")
     code = _float_code(out, "out")
-    stats = _TokenStats(_at(saved["logit_max"]), _at(saved["log_sum"]), None, _at(entropy),
-                        _at(saved["flags"]), _at(top_id), None)
+    stats = _TokenStats(_at(logit_max), _at(log_sum), None, _at(entropy), _at(flags), _at(top_id),
+                        None)
     st = lib.sts_token_logprobs_backward(
         ctypes.byref(rows), ctypes.byref(stats), _at(grad_logprob), _at(grad_entropy),
         _at(grad_top), out.data_ptr(), code, out.stride(0) if T > 1 else V, _raw_stream(index))

@@ -226,6 +226,19 @@ def test_binding_refusals():
         sts.sts_token_logprobs(z, None, top_n=-1)
 
 
+@pytest.mark.parametrize("lost,given", [("entropy", "grad_entropy"), ("top_id", "grad_top"), ("flags", None), ("log_sum", None)])
+def test_the_gradient_says_what_the_saved_scalars_lack(lost, given):
+    T, V, n = 3, 50, 2
+    saved = dict(logit_max=torch.zeros(T), log_sum=torch.zeros(T), flags=torch.zeros(T, dtype=torch.int32), entropy=torch.zeros(T),
+                 top_id=torch.zeros(T, n, dtype=torch.int64))
+    grads = dict(grad_entropy=torch.zeros(T), grad_top=torch.zeros(T, n))
+    for broken in ({k: v for k, v in saved.items() if k != lost}, dict(saved, **{lost: None})):
+        with pytest.raises(sts.StsError) as e:
+            sts.sts_token_logprobs_backward(torch.zeros(T, V), torch.zeros(T, dtype=torch.int64), broken, torch.zeros(T),
+                                            **({given: grads[given]} if given else {}))
+        assert e.value.status == NULL and lost in str(e.value)
+
+
 @pytest.mark.parametrize("top_n", [-1, 65, 10 ** 9, 10 ** 12])
 def test_too_many_alternatives_are_refused_before_they_are_allocated(top_n):
     with pytest.raises(sts.StsError) as e:
